@@ -1,0 +1,66 @@
+// Launch arguments shared by the C ABI and the kernels of the operators around
+// the sparse path (norm + rotation, paged decode, window attention).
+#pragma once
+
+#include "common.cuh"
+
+namespace msa {
+
+struct NormRopeArgs {
+  const __nv_bfloat16* src[3];   // q, k, v (v: paged form only, copied)
+  int64_t ss_b[3], ss_t[3], ss_h[3];
+  __nv_bfloat16* dst[3];         // q_out, k_out (dense) or the K / V pages
+  int64_t ds_b[3], ds_t[3], ds_h[3];   // paged k, v: ds_b is the page stride
+  const float* w[2];             // may be null: ones
+  const float* table;            // [n_pos, rot]: rot / 2 cosines, rot / 2 sines
+  const int64_t* positions;      // [B, T], null: pos0 + i
+  int64_t n_pos, pos0, batch, n_tok, n_items;
+  const int32_t* block_table;    // paged form: [B, table_stride]
+  int64_t table_stride, n_pages;
+  int32_t page_size;
+  int32_t heads[3];              // h_q, h_k, h_k (0 without v)
+  int32_t chunks[3];             // ceil(heads / hc)
+  int32_t hc, rot;
+  float eps;
+  int32_t* err;
+};
+
+struct NormRopeBwdArgs {
+  NormRopeArgs f;                 // src: q, k; dst: dx of q, k; w, table, positions, sizes
+  const void* dy[2];              // bf16 or fp32
+  int64_t ys_b[2], ys_t[2], ys_h[2];
+  float* part;                    // [grid, 2, D] weight-gradient sums of each block
+};
+
+struct PagedDecodeArgs {
+  const __nv_bfloat16* q;         // [B, 1, H, 128]
+  int64_t qs_b, qs_h;
+  const int32_t* block_table;     // [B, table_stride]
+  const int32_t* seq_lens;        // [B]
+  int64_t table_stride, n_pages, cap;   // cap: tokens a sequence may have
+  int32_t page_size, batch, G, R;
+  int64_t window, sink;           // window 0: the whole cache
+  float scale;
+  __nv_bfloat16* out;             // [B, 1, H, 128]
+  float* lse;                     // [B, 1, H]
+  int32_t* prefix;                // workspace: [B + 1] tiles before each sequence (per group)
+  float* part_ml;                 // workspace: [workers, 2, R, 2]
+  float* part_acc;                // workspace: [workers, 2, R, 128]
+  int32_t* err;
+};
+
+struct WindowArgs {
+  const __nv_bfloat16 *q, *o, *d_o;   // q: [B, n_q, H, 128]; o, d_o: backward only
+  int64_t qs_b, qs_t, qs_h, os_b, os_t, os_h, ds_b, ds_t, ds_h;
+  int64_t batch, n_q, n_kv, q_pos0;
+  int64_t window, sink;           // visible: j <= t and (t - j < window or j < sink)
+  int32_t G, R;
+  float scale;
+  const int32_t* kv_len;          // [B] or null: queries at positions >= kv_len are padding
+  __nv_bfloat16* out;             // [B, n_q, H, 128]
+  float* lse;                     // [B, n_q, H]
+  __nv_bfloat16 *dq, *dk, *dv;    // backward
+  int32_t* err;
+};
+
+}  // namespace msa

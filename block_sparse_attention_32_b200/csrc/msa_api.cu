@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "layer_args.cuh"
 
 namespace msa {
 cudaError_t launch_index_score_prefill(const CUtensorMap&, const CUtensorMap&, int, int64_t,
@@ -58,6 +59,20 @@ cudaError_t launch_index_score_e4m3(const CUtensorMap&, const CUtensorMap&, int6
                                    const float*, int32_t*, cudaStream_t);
 cudaError_t launch_quantize_e4m3(const void*, int64_t, void*, float*, cudaStream_t);
 uint64_t set_attn_wait_limit(uint64_t);
+cudaError_t launch_norm_rope(NormRopeArgs, int32_t, bool, bool, cudaStream_t);
+size_t norm_rope_bwd_workspace(int32_t);
+cudaError_t launch_norm_rope_bwd(NormRopeBwdArgs, int32_t, bool, bool, float*, float*,
+                                 cudaStream_t);
+size_t paged_decode_workspace(int64_t, int32_t);
+int64_t paged_decode_max_batch();
+int32_t paged_decode_tile();
+cudaError_t launch_paged_decode(const CUtensorMap&, const CUtensorMap&, PagedDecodeArgs, void*,
+                                cudaStream_t);
+cudaError_t launch_window_attn_fwd(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                   const WindowArgs&, cudaStream_t);
+size_t window_attn_bwd_workspace(const WindowArgs&);   // 0: too many work items
+cudaError_t launch_window_attn_bwd(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                   const CUtensorMap&, WindowArgs, void*, cudaStream_t);
 cudaError_t launch_merge(const int32_t*, const float*, const void*, bool, void*, float*,
                          int64_t, int64_t, int32_t, int32_t, int64_t, int32_t*, cudaStream_t);
 }  // namespace msa
@@ -612,6 +627,365 @@ msa_status msa_token_select_attention(const msa_dims* d, msa_tensor q, msa_tenso
       q_idx.s_tok, q_idx.s_head, k.ptr, k.s_batch, k.s_tok, k.s_head, v.ptr, v.s_batch, v.s_tok,
       v.s_head, d->batch, d->n_q, d->n_kv, d->q_pos0, d->h_kv, d->h_q, d->d_idx, d->h_kidx,
       d->scale, budget, tokens, out, lse, ws, dev_err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+msa_status check_norm_rope(const msa_norm_rope_dims* d, const float* w_q, const float* w_k,
+                           const float* table, int64_t n_pos, const int64_t* positions) {
+  if (d == nullptr) return MSA_ERR_INVALID_ARG;
+  if (d->batch < 1 || d->n_tok < 1 || d->pos0 < 0 || d->h_q < 0 || d->h_k < 0)
+    return MSA_ERR_INVALID_ARG;
+  if (d->h_q == 0 && d->h_k == 0) return MSA_ERR_INVALID_ARG;
+  if (!(d->eps >= 0.f) || !std::isfinite(d->eps)) return MSA_ERR_INVALID_ARG;
+  if (d->interleaved != 0 && d->interleaved != 1) return MSA_ERR_INVALID_ARG;
+  if (d->d != 64 && d->d != 128) return MSA_ERR_UNSUPPORTED;
+  if (d->rot < 0 || d->rot > d->d || d->rot % 16 != 0) return MSA_ERR_UNSUPPORTED;
+  // token x head counts in 40 bits: every index below fits 64
+  if (d->batch > (int64_t(1) << 31) || d->n_tok > (int64_t(1) << 31) || d->h_q > 65535 ||
+      d->h_k > 65535 || d->batch * d->n_tok > (int64_t(1) << 31))
+    return MSA_ERR_UNSUPPORTED;
+  if (n_pos < 0 || (d->rot > 0 && table == nullptr)) return MSA_ERR_INVALID_ARG;
+  if (positions == nullptr && d->pos0 > n_pos - d->n_tok) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(table) || !aligned16(w_q) || !aligned16(w_k)) return MSA_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(positions) & 7u) != 0) return MSA_ERR_ALIGNMENT;
+  return MSA_OK;
+}
+
+msa_status check_paged(const msa_paged_kv* c) {
+  if (c == nullptr || c->k == nullptr || c->v == nullptr || c->block_table == nullptr)
+    return MSA_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->table_stride < 1 || c->h_kv < 1) return MSA_ERR_INVALID_ARG;
+  if (c->s_page < 0 || c->s_tok < 0 || c->s_head < 0) return MSA_ERR_INVALID_ARG;
+  // tokens, heads and pages of a cache are places of their own
+  if (c->s_tok == 0 || (c->s_head == 0 && c->h_kv > 1) || (c->s_page == 0 && c->n_pages > 1))
+    return MSA_ERR_INVALID_ARG;
+  if (!is_pow2(c->page_size) || c->page_size < 16 || c->n_pages > 0x7FFFFFFF)
+    return MSA_ERR_UNSUPPORTED;
+  if (!aligned16(c->k) || !aligned16(c->v)) return MSA_ERR_ALIGNMENT;
+  if ((c->s_page % 8) || (c->s_tok % 8) || (c->s_head % 8)) return MSA_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(c->block_table) & 3u) ||
+      (reinterpret_cast<uintptr_t>(c->seq_lens) & 3u))
+    return MSA_ERR_ALIGNMENT;
+  return MSA_OK;
+}
+
+// check_tensor for strides in elements of `bytes` bytes
+msa_status check_rows(const msa_tensor& t, int bytes) {
+  const msa_status s = check_tensor(t);
+  if (s == MSA_OK || bytes == 2 || s != MSA_ERR_ALIGNMENT) return s;
+  const int64_t e = 16 / bytes;
+  if (!aligned16(t.ptr) || t.s_batch % e || t.s_tok % e || t.s_head % e) return MSA_ERR_ALIGNMENT;
+  return MSA_OK;
+}
+
+msa::NormRopeArgs norm_rope_args(const msa_norm_rope_dims* d, const float* w_q, const float* w_k,
+                                 const float* table, int64_t n_pos, const int64_t* positions,
+                                 int32_t* dev_err) {
+  msa::NormRopeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.w[0] = w_q;
+  a.w[1] = w_k;
+  a.table = table;
+  a.positions = positions;
+  a.n_pos = n_pos;
+  a.pos0 = d->pos0;
+  a.batch = d->batch;
+  a.n_tok = d->n_tok;
+  a.heads[0] = d->h_q;
+  a.heads[1] = d->h_k;
+  a.rot = d->rot;
+  a.eps = d->eps;
+  a.page_size = 1;
+  a.err = dev_err;
+  return a;
+}
+void set_src(msa::NormRopeArgs& a, int k, const msa_tensor& t) {
+  a.src[k] = reinterpret_cast<const __nv_bfloat16*>(t.ptr);
+  a.ss_b[k] = t.s_batch;
+  a.ss_t[k] = t.s_tok;
+  a.ss_h[k] = t.s_head;
+}
+void set_dst(msa::NormRopeArgs& a, int k, void* p, int64_t sb, int64_t st, int64_t sh) {
+  a.dst[k] = reinterpret_cast<__nv_bfloat16*>(p);
+  a.ds_b[k] = sb;
+  a.ds_t[k] = st;
+  a.ds_h[k] = sh;
+}
+void set_dst(msa::NormRopeArgs& a, int k, const msa_tensor& t) {
+  set_dst(a, k, const_cast<void*>(t.ptr), t.s_batch, t.s_tok, t.s_head);
+}
+
+// 5-D bf16 view of a paged cache tensor: {64 columns, page_size tokens, 2 panels,
+// heads, pages}; box {64, rows, 2, 1, 1} lands as [panel][rows][128 B]
+msa_status make_map_pages(CUtensorMap* map, const void* ptr, const msa_paged_kv* c,
+                          uint32_t rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return MSA_ERR_CUDA;
+  cuuint64_t dims[5] = {64, (cuuint64_t)c->page_size, 2, (cuuint64_t)c->h_kv,
+                        (cuuint64_t)c->n_pages};
+  cuuint64_t strides[4] = {(cuuint64_t)c->s_tok * 2, 128, (cuuint64_t)c->s_head * 2,
+                           (cuuint64_t)c->s_page * 2};
+  for (int i = 0; i < 4; ++i)
+    if (strides[i] == 0) strides[i] = 16;      // a dimension of extent 1 still needs a stride
+  cuuint32_t box[5] = {64, rows, 2, 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MSA_OK : MSA_ERR_CUDA;
+}
+
+msa::WindowArgs window_args(const msa_dims* d, int64_t window, int64_t n_sink,
+                            const int32_t* kv_len, int32_t* dev_err) {
+  msa::WindowArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.batch = d->batch;
+  a.n_q = d->n_q;
+  a.n_kv = d->n_kv;
+  a.q_pos0 = d->q_pos0;
+  a.window = window;
+  a.sink = msa::min64(n_sink, d->n_kv);
+  a.G = d->h_kv;
+  a.R = d->h_q / d->h_kv;
+  a.scale = d->scale;
+  a.kv_len = kv_len;
+  a.err = dev_err;
+  return a;
+}
+
+// q-shaped [B, n_q, H, 128] tiles: 128 / R queries x R heads, 64 columns a box
+msa_status make_map_rows(CUtensorMap* map, const msa_dims* d, const msa_tensor& t) {
+  const int32_t R = d->h_q / d->h_kv;
+  return make_map(map, t.ptr, MSA_HEAD_DIM, d->h_q, d->n_q, d->batch, t.s_head, t.s_tok,
+                  t.s_batch, (uint32_t)R, (uint32_t)(MSA_BLOCK_TOKENS / R));
+}
+// k, v [B, h_kv, n_kv, 128]: 128 keys, 64 columns a box
+msa_status make_map_keys(CUtensorMap* map, const msa_dims* d, const msa_tensor& t) {
+  return make_map(map, t.ptr, MSA_HEAD_DIM, d->n_kv, d->h_kv, d->batch, t.s_tok, t.s_head,
+                  t.s_batch, MSA_BLOCK_TOKENS, 1);
+}
+
+msa_status check_window(const msa_dims* d, int64_t window, int64_t n_sink,
+                        const int32_t* kv_len) {
+  const msa_status s = check_dims(d);
+  if (s != MSA_OK) return s;
+  if (window < 0 || n_sink < 0) return MSA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(kv_len) & 3u) != 0) return MSA_ERR_ALIGNMENT;
+  return MSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+msa_status msa_qk_norm_rope(const msa_norm_rope_dims* d, msa_tensor q, msa_tensor k,
+                            const float* w_q, const float* w_k, const float* table,
+                            int64_t n_pos, const int64_t* positions, msa_tensor q_out,
+                            msa_tensor k_out, int32_t* dev_err, void* stream) {
+  msa_status s = check_norm_rope(d, w_q, w_k, table, n_pos, positions);
+  if (s != MSA_OK) return s;
+  for (const msa_tensor* t : {&q, &q_out})
+    if (d->h_q > 0 && (s = check_tensor(*t)) != MSA_OK) return s;
+  for (const msa_tensor* t : {&k, &k_out})
+    if (d->h_k > 0 && (s = check_tensor(*t)) != MSA_OK) return s;
+  msa::NormRopeArgs a = norm_rope_args(d, w_q, w_k, table, n_pos, positions, dev_err);
+  set_src(a, 0, q);
+  set_src(a, 1, k);
+  set_dst(a, 0, q_out);
+  set_dst(a, 1, k_out);
+  return from_cuda(msa::launch_norm_rope(a, d->d, d->interleaved != 0, false,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+msa_status msa_qk_norm_rope_paged(const msa_norm_rope_dims* d, msa_tensor q, msa_tensor k,
+                                  msa_tensor v, const float* w_q, const float* w_k,
+                                  const float* table, int64_t n_pos, const int64_t* positions,
+                                  msa_tensor q_out, const msa_paged_kv* cache, int32_t* dev_err,
+                                  void* stream) {
+  msa_status s = check_norm_rope(d, w_q, w_k, table, n_pos, positions);
+  if (s != MSA_OK) return s;
+  if (d->d != MSA_HEAD_DIM) return MSA_ERR_UNSUPPORTED;
+  if ((s = check_paged(cache)) != MSA_OK) return s;
+  if (d->h_k != cache->h_kv) return MSA_ERR_INVALID_ARG;
+  for (const msa_tensor* t : {&q, &q_out})
+    if (d->h_q > 0 && (s = check_tensor(*t)) != MSA_OK) return s;
+  if ((s = check_tensor(k)) != MSA_OK) return s;
+  if ((s = check_tensor(v)) != MSA_OK) return s;
+  msa::NormRopeArgs a = norm_rope_args(d, w_q, w_k, table, n_pos, positions, dev_err);
+  set_src(a, 0, q);
+  set_src(a, 1, k);
+  set_src(a, 2, v);
+  set_dst(a, 0, q_out);
+  set_dst(a, 1, cache->k, cache->s_page, cache->s_tok, cache->s_head);
+  set_dst(a, 2, cache->v, cache->s_page, cache->s_tok, cache->s_head);
+  a.heads[2] = d->h_k;
+  a.block_table = cache->block_table;
+  a.table_stride = cache->table_stride;
+  a.n_pages = cache->n_pages;
+  a.page_size = cache->page_size;
+  return from_cuda(msa::launch_norm_rope(a, d->d, d->interleaved != 0, true,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t msa_qk_norm_rope_bwd_workspace(const msa_norm_rope_dims* d) {
+  if (d == nullptr || (d->d != 64 && d->d != 128)) return 0;
+  return msa::norm_rope_bwd_workspace(d->d);
+}
+
+msa_status msa_qk_norm_rope_bwd(const msa_norm_rope_dims* d, msa_tensor q, msa_tensor k,
+                                const float* w_q, const float* w_k, const float* table,
+                                int64_t n_pos, const int64_t* positions, msa_tensor d_q,
+                                msa_tensor d_k, int32_t dy_fp32, msa_tensor dx_q,
+                                msa_tensor dx_k, float* dw_q, float* dw_k, void* ws,
+                                size_t ws_bytes, int32_t* dev_err, void* stream) {
+  msa_status s = check_norm_rope(d, w_q, w_k, table, n_pos, positions);
+  if (s != MSA_OK) return s;
+  if (dy_fp32 != 0 && dy_fp32 != 1) return MSA_ERR_INVALID_ARG;
+  for (const msa_tensor* t : {&q, &dx_q})
+    if (d->h_q > 0 && (s = check_tensor(*t)) != MSA_OK) return s;
+  for (const msa_tensor* t : {&k, &dx_k})
+    if (d->h_k > 0 && (s = check_tensor(*t)) != MSA_OK) return s;
+  if (d->h_q > 0 && (s = check_rows(d_q, dy_fp32 ? 4 : 2)) != MSA_OK) return s;
+  if (d->h_k > 0 && (s = check_rows(d_k, dy_fp32 ? 4 : 2)) != MSA_OK) return s;
+  if (ws == nullptr) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(ws)) return MSA_ERR_ALIGNMENT;
+  if (ws_bytes < msa_qk_norm_rope_bwd_workspace(d)) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  msa::NormRopeBwdArgs p;
+  std::memset(&p, 0, sizeof(p));
+  p.f = norm_rope_args(d, w_q, w_k, table, n_pos, positions, dev_err);
+  set_src(p.f, 0, q);
+  set_src(p.f, 1, k);
+  set_dst(p.f, 0, dx_q);
+  set_dst(p.f, 1, dx_k);
+  const msa_tensor* dy[2] = {&d_q, &d_k};
+  for (int i = 0; i < 2; ++i) {
+    p.dy[i] = dy[i]->ptr;
+    p.ys_b[i] = dy[i]->s_batch;
+    p.ys_t[i] = dy[i]->s_tok;
+    p.ys_h[i] = dy[i]->s_head;
+  }
+  p.part = reinterpret_cast<float*>(ws);
+  return from_cuda(msa::launch_norm_rope_bwd(p, d->d, d->interleaved != 0, dy_fp32 != 0, dw_q,
+                                             dw_k, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t msa_paged_decode_attn_workspace(const msa_dims* d) {
+  if (check_dims(d) != MSA_OK) return 0;
+  return msa::paged_decode_workspace(d->batch, d->h_q / d->h_kv);
+}
+
+msa_status msa_paged_decode_attn(const msa_dims* d, int64_t window, int64_t n_sink, msa_tensor q,
+                                 const msa_paged_kv* cache, void* out, float* lse, void* ws,
+                                 size_t ws_bytes, int32_t* dev_err, void* stream) {
+  msa_status s = check_dims(d);
+  if (s != MSA_OK) return s;
+  if (d->n_q != 1 || window < 0 || n_sink < 0) return MSA_ERR_INVALID_ARG;
+  if ((s = check_tensor(q)) != MSA_OK) return s;
+  if ((s = check_paged(cache)) != MSA_OK) return s;
+  if (cache->seq_lens == nullptr || cache->h_kv != d->h_kv) return MSA_ERR_INVALID_ARG;
+  if (cache->table_stride < (d->n_kv + cache->page_size - 1) / cache->page_size)
+    return MSA_ERR_INVALID_ARG;
+  if (out == nullptr || lse == nullptr || ws == nullptr) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(ws) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return MSA_ERR_ALIGNMENT;
+  if (ws_bytes < msa_paged_decode_attn_workspace(d)) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  const int32_t tile = msa::paged_decode_tile();
+  if (d->batch > msa::paged_decode_max_batch() ||
+      d->batch * d->h_kv * (d->n_kv / tile + 2) > 0x7FFFFFFF)
+    return MSA_ERR_UNSUPPORTED;
+  CUtensorMap tk, tv;
+  const uint32_t rows = (uint32_t)(cache->page_size < tile ? cache->page_size : tile);
+  if ((s = make_map_pages(&tk, cache->k, cache, rows)) != MSA_OK) return s;
+  if ((s = make_map_pages(&tv, cache->v, cache, rows)) != MSA_OK) return s;
+  msa::PagedDecodeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q.ptr);
+  a.qs_b = q.s_batch;
+  a.qs_h = q.s_head;
+  a.block_table = cache->block_table;
+  a.seq_lens = cache->seq_lens;
+  a.table_stride = cache->table_stride;
+  a.n_pages = cache->n_pages;
+  a.cap = d->n_kv;
+  a.page_size = cache->page_size;
+  a.batch = (int32_t)d->batch;
+  a.G = d->h_kv;
+  a.R = d->h_q / d->h_kv;
+  a.window = window;
+  a.sink = msa::min64(n_sink, d->n_kv);
+  a.scale = d->scale;
+  a.out = reinterpret_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.err = dev_err;
+  return from_cuda(
+      msa::launch_paged_decode(tk, tv, a, ws, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+msa_status msa_window_attn_fwd(const msa_dims* d, int64_t window, int64_t n_sink, msa_tensor q,
+                               msa_tensor k, msa_tensor v, const int32_t* kv_len, void* out,
+                               float* lse, int32_t* dev_err, void* stream) {
+  msa_status s = check_window(d, window, n_sink, kv_len);
+  if (s != MSA_OK) return s;
+  for (const msa_tensor* t : {&q, &k, &v})
+    if ((s = check_tensor(*t)) != MSA_OK) return s;
+  if (out == nullptr || lse == nullptr) return MSA_ERR_INVALID_ARG;
+  if (!aligned32(out) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return MSA_ERR_ALIGNMENT;
+  CUtensorMap tq, tk, tv;
+  if ((s = make_map_rows(&tq, d, q)) != MSA_OK) return s;
+  if ((s = make_map_keys(&tk, d, k)) != MSA_OK) return s;
+  if ((s = make_map_keys(&tv, d, v)) != MSA_OK) return s;
+  msa::WindowArgs a = window_args(d, window, n_sink, kv_len, dev_err);
+  a.out = reinterpret_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  return from_cuda(msa::launch_window_attn_fwd(tq, tk, tv, a,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t msa_window_attn_bwd_workspace(const msa_dims* d, int64_t window, int64_t n_sink) {
+  if (check_window(d, window, n_sink, nullptr) != MSA_OK) return 0;
+  return msa::window_attn_bwd_workspace(window_args(d, window, n_sink, nullptr, nullptr));
+}
+
+msa_status msa_window_attn_bwd(const msa_dims* d, int64_t window, int64_t n_sink, msa_tensor q,
+                               msa_tensor k, msa_tensor v, msa_tensor o, msa_tensor d_o,
+                               const float* lse, const int32_t* kv_len, void* dq, void* dk,
+                               void* dv, void* ws, size_t ws_bytes, int32_t* dev_err,
+                               void* stream) {
+  msa_status s = check_window(d, window, n_sink, kv_len);
+  if (s != MSA_OK) return s;
+  for (const msa_tensor* t : {&q, &k, &v, &o, &d_o})
+    if ((s = check_tensor(*t)) != MSA_OK) return s;
+  if (lse == nullptr || dq == nullptr || dk == nullptr || dv == nullptr || ws == nullptr)
+    return MSA_ERR_INVALID_ARG;
+  if (!aligned32(dq) || !aligned32(dk) || !aligned32(dv) || !aligned32(ws) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return MSA_ERR_ALIGNMENT;
+  const size_t need = msa_window_attn_bwd_workspace(d, window, n_sink);
+  if (need == 0) return MSA_ERR_UNSUPPORTED;
+  if (ws_bytes < need) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  CUtensorMap tq, tdo, tk, tv;
+  if ((s = make_map_rows(&tq, d, q)) != MSA_OK) return s;
+  if ((s = make_map_rows(&tdo, d, d_o)) != MSA_OK) return s;
+  if ((s = make_map_keys(&tk, d, k)) != MSA_OK) return s;
+  if ((s = make_map_keys(&tv, d, v)) != MSA_OK) return s;
+  msa::WindowArgs a = window_args(d, window, n_sink, kv_len, dev_err);
+  a.o = reinterpret_cast<const __nv_bfloat16*>(o.ptr);
+  a.os_b = o.s_batch;
+  a.os_t = o.s_tok;
+  a.os_h = o.s_head;
+  a.d_o = reinterpret_cast<const __nv_bfloat16*>(d_o.ptr);
+  a.ds_b = d_o.s_batch;
+  a.ds_t = d_o.s_tok;
+  a.ds_h = d_o.s_head;
+  a.lse = const_cast<float*>(lse);
+  a.dq = reinterpret_cast<__nv_bfloat16*>(dq);
+  a.dk = reinterpret_cast<__nv_bfloat16*>(dk);
+  a.dv = reinterpret_cast<__nv_bfloat16*>(dv);
+  return from_cuda(msa::launch_window_attn_bwd(tq, tdo, tk, tv, a, ws,
+                                               reinterpret_cast<cudaStream_t>(stream)));
 }
 
 uint64_t msa_debug_set_attn_wait_limit_ns(uint64_t ns) {

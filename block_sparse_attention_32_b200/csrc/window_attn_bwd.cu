@@ -1,0 +1,760 @@
+// Backward of the window attention (window_attn.cu).  With p_ij = e^{scale q_i.k_j -
+// lse_i} over the keys J(t_i) that query i sees, D_i = dO_i.o_i and
+// dS_ij = p_ij (dO_i.v_j - D_i):
+//   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i p_ij dO_i,
+// the last two over every query and every head of the group that sees key j.
+//
+// Bound: the tensor cores.  One pass over (query, key) tiles would need five
+// products a tile but leaves one of dq and dk, dv to be added up across CTAs:
+// dq pieces of every (row, key block) cost more HBM time (W / 128 pieces of 512
+// bytes a row, written and read) than products, and atomics would make the bits
+// depend on their order.  So each output gets its own walk, 4 + 3 products a
+// tile pair, and every sum stays in TMEM in a fixed order:
+//   dk, dv item  keys = the 128 accumulator rows, K and V stay; Q and dO tiles
+//                stream: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
+//   dq item      query rows stay (Q, dO); K and V tiles stream:
+//                S = Q K^T, dP = dO V^T, dQ += dS K
+// Both are "stay x stream" products of one shape, so ONE persistent kernel runs
+// both kinds of item through the same roles, dealt by a counter: the short dq
+// items fill the tail that the long dk, dv items leave.  Which CTA takes an item
+// changes no result.
+//   warps 0-3, 4-7  P and dS: thread = accumulator row, columns 0-63 / 64-127
+//   warp 8          scheduler and TMA;  warp 9  MMA;  warp 10  -lse, -D of the
+//                   streamed rows;  warp 11 idle
+// TMEM: S (P in place, bf16), dP (dS in place), dV, dK or dQ: 128 columns each.
+// Per tile the tensor core runs dP(n), dV(n), S(n+1), dK(n): the exponentials of
+// n+1 run under dK(n) and dP(n+1), the dS of n under dV(n) and S(n+1).
+// A key block that many queries see (sinks; no window) is cut into chunks of
+// query tiles whose fp32 sums a last kernel adds in chunk order.
+#include "common.cuh"
+#include "layer_args.cuh"
+#include "window_tiles.cuh"
+
+namespace msa {
+
+namespace {
+constexpr int kWbThreads = 384;
+constexpr int kWbRegsAtLaunch = 168, kWbRegsControl = 104, kWbRegsMath = 200;
+static_assert(kWbRegsControl + 2 * kWbRegsMath == 3 * kWbRegsAtLaunch,
+              "warpgroup register shares must add up to the launch allocation");
+constexpr int kWbOffStay = 0;                          // K, V or Q, dO: 32 KB each
+constexpr int kWbOffStream = 65536;                    // two slots of 64 KB
+constexpr int kWbOffMeta = kWbOffStream + 2 * 65536;   // two slots: -lse log2 e [128], -D [128]
+constexpr int kWbOffBar = kWbOffMeta + 2 * 1024;
+enum {
+  XB_ITEM_FULL = 0, XB_ITEM_EMPTY = 2, XB_STAY_FULL = 4, XB_STAY_EMPTY, XB_STR_FULL = 6,
+  XB_STR_EMPTY = 8, XB_META_FULL = 10, XB_S_FULL = 12, XB_DP_FULL, XB_P_FULL, XB_DS_FULL, XB_DV_DONE, XB_DK_DONE,
+  XB_ACC_FULL, XB_ACC_EMPTY, XB_DRAIN, XB_COUNT
+};
+constexpr int kWbOffMisc = kWbOffBar + XB_COUNT * 8;
+constexpr int kWbSmemBytes = 1024 + kWbOffMisc + 32;
+static_assert(kWbSmemBytes <= 232448, "shared memory per block");
+constexpr int kWbItemReaders = 10;     // warps that read an item's number: 0-7, 9, 10
+constexpr int kWbMinChunk = 32;        // query tiles of a chunk at least
+constexpr int kWbSplit = 2 * 148;      // chunks aimed at when blocks are cut
+
+struct WindowBwdArgs {
+  WindowArgs w;
+  const float* delta;       // [B, n_q, H]
+  const int2* table;        // [n_cut]: (key block, chunk), the same for every (batch, group)
+  const int32_t* pbase;     // [nblk]: first partial of a cut block, -1 for an uncut one
+  int32_t* counter;
+  float* part;              // [B * G, n_part, 2, 128, 128]: dV, dK sums of a chunk
+  int32_t chunk, nblk, n_cut, n_part, n_dkv, n_all;
+};
+
+// query tiles (128 / R tokens) that see key block c: [first, first + count)
+__host__ __device__ __forceinline__ void wb_query_tiles(const WindowArgs& a, int64_t c,
+                                                        int32_t& first, int32_t& count) {
+  const int64_t k0 = c * 128, tpt = 128 / a.R;
+  const int64_t lo = max64(0, k0 - a.q_pos0);
+  int64_t hi = a.n_q - 1;
+  if (a.window > 0 && k0 >= a.sink)
+    hi = min64(hi, k0 + 126 - a.q_pos0 + min64(a.window, int64_t(1) << 40));
+  first = (int32_t)(lo / tpt);
+  count = hi < lo ? 0 : (int32_t)(hi / tpt) - first + 1;
+}
+__host__ __device__ __forceinline__ int32_t wb_chunks(int32_t count, int32_t chunk) {
+  return count <= chunk ? 1 : (count + chunk - 1) / chunk;
+}
+
+struct WbPlan {
+  int64_t nblk, n_cut, n_part, c_lo, c_hi, n_dkv, n_dq;   // c_lo .. c_hi: the cut blocks' range
+  int32_t chunk;
+};
+WbPlan wb_plan(const WindowArgs& a) {
+  WbPlan p{};
+  p.nblk = (a.n_kv + 127) / 128;
+  int64_t total = 0;
+  for (int64_t c = 0; c < p.nblk; ++c) {
+    int32_t f, n;
+    wb_query_tiles(a, c, f, n);
+    total += n;
+  }
+  p.chunk = (int32_t)max64(kWbMinChunk, (total * a.batch * a.G + kWbSplit - 1) / kWbSplit);
+  p.c_lo = p.nblk;
+  for (int64_t c = 0; c < p.nblk; ++c) {
+    int32_t f, n;
+    wb_query_tiles(a, c, f, n);
+    const int32_t k = wb_chunks(n, p.chunk);
+    p.n_cut += k;
+    if (k > 1) {
+      p.n_part += k;
+      p.c_lo = min64(p.c_lo, c);
+      p.c_hi = c + 1;
+    }
+  }
+  p.n_dkv = p.n_cut * a.batch * a.G;
+  p.n_dq = a.batch * a.G * ((a.n_q * a.R + 127) / 128);
+  return p;
+}
+size_t pad32(size_t n) { return (n + 31) / 32 * 32; }
+
+// one work item, as every role sees it
+struct WbItem {
+  bool dkv;
+  int32_t b, g, nt;          // nt: streamed tiles
+  int32_t k0, q_tile, part;  // dkv: first key, first query tile, partial (-1: final)
+  int32_t len;
+  WinItem w;                 // dq
+};
+__device__ __forceinline__ void wb_item(WbItem& it, const WindowBwdArgs& p, int32_t idx) {
+  const WindowArgs& a = p.w;
+  const int32_t bg_all = (int32_t)a.batch * a.G;
+  it.dkv = idx < p.n_dkv;
+  if (it.dkv) {
+    const int32_t e = idx / bg_all, bg = idx - e * bg_all;
+    it.b = bg / a.G;
+    it.g = bg - it.b * a.G;
+    const int2 t = __ldg(p.table + e);
+    int32_t first, count;
+    wb_query_tiles(a, t.x, first, count);
+    const int32_t k = wb_chunks(count, p.chunk);
+    const int32_t q0 = (int32_t)((int64_t)count * t.y / k);
+    int32_t q1 = (int32_t)((int64_t)count * (t.y + 1) / k);
+    it.k0 = t.x * 128;
+    it.q_tile = first + q0;
+    it.part = k > 1 ? bg * p.n_part + __ldg(p.pbase + t.x) + t.y : -1;
+    it.len = win_len(a, it.b);
+    const int64_t live = (int64_t)it.len - a.q_pos0;         // queries before the padding
+    const int32_t tpt = 128 / a.R;
+    const int32_t end = live <= 0 || it.k0 >= it.len ? 0 : (int32_t)((live + tpt - 1) / tpt);
+    it.nt = max(0, min(q1 - q0, end - it.q_tile));
+  } else {
+    win_item(it.w, a, idx - p.n_dkv, 1);
+    it.b = it.w.b;
+    it.g = it.w.g;
+    it.nt = it.w.nt;
+    it.len = it.w.len;
+  }
+}
+
+// columns lo .. hi - 1 of the 64 from c0 on, as bits
+__device__ __forceinline__ uint64_t range_bits(int32_t lo, int32_t hi, int32_t c0) {
+  lo = max(lo - c0, 0);
+  hi = min(hi - c0, 64);
+  if (lo >= hi) return 0ull;
+  return (hi >= 64 ? ~0ull : (1ull << hi) - 1) & ~((1ull << lo) - 1);
+}
+}  // namespace
+
+// D = dO.o of every row, a warp each; the last block lays out the cut key blocks
+// and sets the item counter back
+__global__ void __launch_bounds__(256)
+    window_bwd_prep_kernel(const __grid_constant__ WindowArgs a, float* __restrict__ delta,
+                           int2* __restrict__ table, int32_t* __restrict__ pbase,
+                           int32_t* __restrict__ counter, int32_t chunk, int32_t nblk) {
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x + 1 < gridDim.x) {
+    const int64_t H = (int64_t)a.G * a.R;
+    const int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    if (r >= a.batch * a.n_q * H) return;
+    const int64_t h = r % H, bt = r / H, b = bt / a.n_q, t = bt - b * a.n_q;
+    const uint2 ov = *reinterpret_cast<const uint2*>(a.o + b * a.os_b + t * a.os_t + h * a.os_h +
+                                                     4 * lane);
+    const uint2 dv = *reinterpret_cast<const uint2*>(a.d_o + b * a.ds_b + t * a.ds_t +
+                                                     h * a.ds_h + 4 * lane);
+    const float2 o0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ov.x));
+    const float2 o1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ov.y));
+    const float2 d0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&dv.x));
+    const float2 d1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&dv.y));
+    float s = o0.x * d0.x + o0.y * d0.y + o1.x * d1.x + o1.y * d1.y;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    if (lane == 0) delta[r] = s;
+    return;
+  }
+  __shared__ int2 wsum[8], carry;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) {
+    *counter = 0;
+    carry = make_int2(0, 0);
+  }
+  for (int32_t c0 = 0; c0 < nblk; c0 += 256) {
+    const int32_t c = c0 + tid;
+    int32_t first, count = 0, k = 0;
+    if (c < nblk) {
+      wb_query_tiles(a, c, first, count);
+      k = wb_chunks(count, chunk);
+    }
+    int2 inc = make_int2(k, k > 1 ? k : 0);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc.x, o);
+      const int y = __shfl_up_sync(0xffffffffu, inc.y, o);
+      if (lane >= o) {
+        inc.x += x;
+        inc.y += y;
+      }
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int2 off = carry;
+    for (int w = 0; w < warp; ++w) {
+      off.x += wsum[w].x;
+      off.y += wsum[w].y;
+    }
+    if (c < nblk) {
+      const int32_t e = off.x + inc.x - k;
+      for (int32_t j = 0; j < k; ++j) table[e + j] = make_int2(c, j);
+      pbase[c] = k > 1 ? off.y + inc.y - k : -1;
+    }
+    __syncthreads();
+    if (tid == 255) carry = make_int2(off.x + inc.x, off.y + inc.y);
+    __syncthreads();
+  }
+}
+
+__global__ void __launch_bounds__(kWbThreads, 1)
+    window_attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q,
+                           const __grid_constant__ CUtensorMap tm_do,
+                           const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v,
+                           const __grid_constant__ WindowBwdArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(base + kWbOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + kWbOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + kWbOffMisc + 4);
+  volatile int32_t* item_slot = reinterpret_cast<volatile int32_t*>(base + kWbOffMisc + 8);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const WindowArgs& a = p.w;
+  int32_t* err = a.err;
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar + XB_ITEM_FULL + s, 1);
+      mbar_init(bar + XB_ITEM_EMPTY + s, kWbItemReaders);
+      mbar_init(bar + XB_STR_FULL + s, 1);
+      mbar_init(bar + XB_STR_EMPTY + s, 1);
+      mbar_init(bar + XB_META_FULL + s, 1);
+    }
+    mbar_init(bar + XB_STAY_FULL, 1);
+    mbar_init(bar + XB_STAY_EMPTY, 1);
+    mbar_init(bar + XB_S_FULL, 1);
+    mbar_init(bar + XB_DP_FULL, 1);
+    mbar_init(bar + XB_P_FULL, 256);
+    mbar_init(bar + XB_DS_FULL, 256);
+    mbar_init(bar + XB_DV_DONE, 1);
+    mbar_init(bar + XB_DK_DONE, 1);
+    mbar_init(bar + XB_ACC_FULL, 1);
+    mbar_init(bar + XB_ACC_EMPTY, 256);
+    mbar_init(bar + XB_DRAIN, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;          // S, dP, dV, dK or dQ: 128 columns each
+  // k-th completion of a barrier has parity k & 1; the whole warp decides together
+  auto W = [&](int id, int64_t k) {
+    return __all_sync(0xffffffffu,
+                      mbar_wait(bar + id, (uint32_t)(k & 1), abort_flag, err));
+  };
+  // the k-th item's number for a reading warp (-1: no more)
+  auto next_item = [&](int64_t k, int32_t& idx) {
+    if (!W(XB_ITEM_FULL + (int)(k & 1), k >> 1)) return false;
+    idx = item_slot[k & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar + XB_ITEM_EMPTY + (int)(k & 1));
+    return idx >= 0;
+  };
+  const int32_t tpt = 128 / a.R;             // tokens per query tile
+  const float log2e = 1.4426950408889634f;
+  WbItem it;
+
+  if (warp >= 8) {
+    setmaxnreg_dec<kWbRegsControl>();
+    if (warp == 8) {
+      // ---------------- scheduler, TMA ----------------
+      if (lane == 0) {
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_do);
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+      }
+      int64_t n = 0, ni = 0;                 // streamed tiles, items with tiles
+      bool ok = true;
+      auto load_rows = [&](uint8_t* dst, uint64_t* b, int32_t tile) {
+        for (int h = 0; h < 2; ++h) {
+          tma_load_4d(dst + h * 16384, &tm_q, b, h * 64, it.g * a.R, tile * tpt, it.b);
+          tma_load_4d(dst + 32768 + h * 16384, &tm_do, b, h * 64, it.g * a.R, tile * tpt, it.b);
+        }
+      };
+      auto load_keys = [&](uint8_t* dst, uint64_t* b, int32_t key0) {
+        for (int h = 0; h < 2; ++h) {
+          tma_load_4d(dst + h * 16384, &tm_k, b, h * 64, key0, it.g, it.b);
+          tma_load_4d(dst + 32768 + h * 16384, &tm_v, b, h * 64, key0, it.g, it.b);
+        }
+      };
+      for (int64_t k = 0; ok; ++k) {
+        if (k >= 2 && !W(XB_ITEM_EMPTY + (int)(k & 1), (k >> 1) - 1)) break;
+        int32_t idx = 0;
+        if (lane == 0) {
+          idx = atomicAdd(p.counter, 1);
+          if (idx >= p.n_all) idx = -1;
+          item_slot[k & 1] = idx;
+          mbar_arrive(bar + XB_ITEM_FULL + (int)(k & 1));
+        }
+        idx = __shfl_sync(0xffffffffu, idx, 0);
+        if (idx < 0) break;
+        wb_item(it, p, idx);
+        if (it.nt == 0) continue;
+        if (ni > 0 && !W(XB_STAY_EMPTY, ni - 1)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar + XB_STAY_FULL, 65536u);
+          if (it.dkv) load_keys(base + kWbOffStay, bar + XB_STAY_FULL, it.k0);
+          else load_rows(base + kWbOffStay, bar + XB_STAY_FULL, it.w.i0 / tpt);
+        }
+        ++ni;
+        for (int32_t t = 0; t < it.nt; ++t, ++n) {
+          const int s = (int)(n & 1);
+          if (n >= 2 && !W(XB_STR_EMPTY + s, (n >> 1) - 1)) { ok = false; break; }
+          if (lane == 0) {
+            uint8_t* dst = base + kWbOffStream + s * 65536;
+            mbar_arrive_expect_tx(bar + XB_STR_FULL + s, 65536u);
+            if (it.dkv) load_rows(dst, bar + XB_STR_FULL + s, it.q_tile + t);
+            else load_keys(dst, bar + XB_STR_FULL + s, win_key0(it.w, t));
+          }
+        }
+      }
+      // no copy may still be writing shared memory when the block exits
+      if (lane == 0) {
+        for (int64_t k = n > 2 ? n - 2 : 0; k < n; ++k)
+          mbar_drain(bar + XB_STR_FULL + (int)(k & 1), (uint32_t)((k >> 1) & 1), err);
+        if (ni > 0) mbar_drain(bar + XB_STAY_FULL, (uint32_t)((ni - 1) & 1), err);
+      }
+    } else if (warp == 9) {
+      // ---------------- MMA ----------------
+      constexpr uint32_t kIdT = idesc_bf16_f32(128, 128, 0), kIdA = idesc_bf16_f32(128, 128, 1);
+      const uint32_t sa = smem_u32(base + kWbOffStay);
+      int64_t n = 0, ni = 0, nv = 0;         // tiles, items with tiles, dV products
+      int32_t idx;
+      // D = X Y^T of two 128 x 128 tiles in shared memory
+      auto mma_t = [&](uint32_t d, uint32_t xa, uint32_t ya) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          umma_bf16(d, smem_desc_sw128(xa + off, 16, 1024), smem_desc_sw128(ya + off, 16, 1024),
+                    kIdT, kk > 0 ? 1u : 0u);
+        }
+      };
+      // D (+)= X Y, X (bf16, two halves of 64) in TMEM, Y in shared memory
+      auto mma_acc = [&](uint32_t d, uint32_t x, uint32_t ya, bool add) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_bf16_ts(d, x + (kk >> 2) * 64 + (kk & 3) * 8,
+                       smem_desc_sw128(ya + kk * 2048, 16384, 1024), kIdA,
+                       add || kk > 0 ? 1u : 0u);
+      };
+      // slot of tile t (number m): copies landed, rows past the sequence cleared:
+      // they may hold anything, and their P and dS are 0, but 0 * NaN is not
+      auto landed = [&](int32_t t, int64_t m) {
+        const int s = (int)(m & 1);
+        if (!W(XB_STR_FULL + s, m >> 1)) return false;
+        uint8_t* tile = base + kWbOffStream + s * 65536;
+        if (it.dkv) {
+          const int64_t r0 =
+              ((int64_t)it.len - a.q_pos0 - (int64_t)(it.q_tile + t) * tpt) * a.R;
+          if (it.len < a.n_kv && r0 < 128) {
+            win_clear_rows(tile, (int32_t)r0, lane);
+            win_clear_rows(tile + 32768, (int32_t)r0, lane);
+          }
+        } else {
+          const int32_t k0 = win_key0(it.w, t);
+          if (it.len < a.n_kv && k0 + 128 > it.len) win_clear_rows(tile, it.len - k0, lane);
+        }
+        return true;
+      };
+      auto issue_s = [&](int64_t m) {
+        tc_fence_after();
+        if (lane == 0) {
+          mma_t(tmem, sa, smem_u32(base + kWbOffStream + (int)(m & 1) * 65536));
+          umma_commit(bar + XB_S_FULL);
+        }
+        __syncwarp();
+      };
+      bool ok = true;
+      for (int64_t k = 0; ok && next_item(k, idx); ++k) {
+        wb_item(it, p, idx);
+        if (it.nt == 0) continue;
+        ok = W(XB_STAY_FULL, ni) && landed(0, n) && (nv == 0 || W(XB_DV_DONE, nv - 1));
+        if (!ok) break;
+        issue_s(n);
+        for (int32_t t = 0; t < it.nt; ++t, ++n) {
+          const uint32_t str = smem_u32(base + kWbOffStream + (int)(n & 1) * 65536);
+          const bool last = t + 1 == it.nt;
+          // dP overwrites the columns dS was read from
+          if (n > 0 && !W(XB_DK_DONE, n - 1)) { ok = false; break; }
+          tc_fence_after();
+          if (lane == 0) {
+            mma_t(tmem + 128, sa + 32768, str + 32768);
+            umma_commit(bar + XB_DP_FULL);
+            if (last) umma_commit(bar + XB_STAY_EMPTY);
+          }
+          __syncwarp();
+          if (!W(XB_P_FULL, n)) { ok = false; break; }
+          if (t == 0 && ni > 0 && !W(XB_ACC_EMPTY, ni - 1)) { ok = false; break; }
+          tc_fence_after();
+          if (it.dkv) {
+            if (lane == 0) {
+              mma_acc(tmem + 256, tmem, str + 32768, t > 0);
+              umma_commit(bar + XB_DV_DONE);
+            }
+            __syncwarp();
+            ++nv;
+          }
+          if (!last) {                        // S overwrites the columns P was read from
+            if (!landed(t + 1, n + 1) || (it.dkv && !W(XB_DV_DONE, nv - 1))) { ok = false; break; }
+            issue_s(n + 1);
+          }
+          if (!W(XB_DS_FULL, n)) { ok = false; break; }
+          tc_fence_after();
+          if (lane == 0) {
+            mma_acc(tmem + 384, tmem + 128, str, t > 0);
+            umma_commit(bar + XB_STR_EMPTY + (int)(n & 1));
+            umma_commit(bar + XB_DK_DONE);
+            if (last) umma_commit(bar + XB_ACC_FULL);
+          }
+          __syncwarp();
+        }
+        ++ni;
+      }
+      // every MMA issued has finished before the tensor memory is freed
+      if (lane == 0) {
+        umma_commit(bar + XB_DRAIN);
+        mbar_drain(bar + XB_DRAIN, 0, err);
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      // ---------------- -lse log2 e and -D of the streamed query rows ----------------
+      int64_t n = 0;
+      int32_t idx;
+      bool ok = true;
+      for (int64_t k = 0; ok && next_item(k, idx); ++k) {
+        wb_item(it, p, idx);
+        for (int32_t t = 0; t < it.nt; ++t, ++n) {
+          const int s = (int)(n & 1);
+          if (n >= 2 && !W(XB_STR_EMPTY + s, (n >> 1) - 1)) { ok = false; break; }
+          if (it.dkv) {
+            float* m = reinterpret_cast<float*>(base + kWbOffMeta + s * 1024);
+            for (int r = lane; r < 128; r += 32) {
+              const int64_t i = (int64_t)(it.q_tile + t) * tpt + r / a.R;
+              const bool live = i < a.n_q && a.q_pos0 + i < it.len;
+              const int64_t row =
+                  ((int64_t)it.b * a.n_q + i) * ((int64_t)a.G * a.R) + it.g * a.R + r % a.R;
+              // padding: p = 2^{0 - inf} = 0
+              m[r] = live ? -log2e * __ldg(a.lse + row) : -INFINITY;
+              m[128 + r] = live ? -__ldg(p.delta + row) : 0.f;
+            }
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(bar + XB_META_FULL + s);
+        }
+      }
+    }
+  } else {
+    setmaxnreg_inc<kWbRegsMath>();
+    // ---------------- P, dS; outputs ----------------
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane, c0 = 64 * half;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_base + c0;
+    const float scale_log2 = a.scale * log2e;
+    const uint64_t scale2 = pack_f32x2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
+    const int64_t H = (int64_t)a.G * a.R;
+    int64_t n = 0, ni = 0;
+    int32_t idx;
+    bool ok = true;
+    for (int64_t k = 0; ok && next_item(k, idx); ++k) {
+      wb_item(it, p, idx);
+      // dq: this thread's query row
+      const int32_t i_row = it.dkv ? 0 : it.w.i0 + row / a.R;
+      const int32_t pos = it.dkv ? it.k0 + row : it.w.q_pos0 + i_row;   // key or query position
+      const int64_t qrow = ((int64_t)it.b * a.n_q + i_row) * H + (int64_t)it.g * a.R + row % a.R;
+      float nl = 0.f, nd = 0.f;
+      const bool row_live = !it.dkv && i_row < a.n_q && pos < it.len;
+      if (row_live) {
+        nl = -log2e * __ldg(a.lse + qrow);
+        nd = -__ldg(p.delta + qrow);
+      }
+      const int32_t win = a.window > 0 ? (int32_t)min64(a.window, int64_t(1) << 30) : 1 << 30;
+      for (int32_t t = 0; t < it.nt; ++t, ++n) {
+        // visible columns of this thread's 64, as bits
+        uint64_t vis;
+        if (it.dkv) {                         // columns: rows of query tile q_tile + t
+          const int32_t t0 = (int32_t)a.q_pos0 + (it.q_tile + t) * tpt;
+          const int32_t lo = (pos - t0) * a.R;
+          const int32_t d = pos + win - t0;   // first query (of the tile) past the window
+          vis = range_bits(pos - t0 > tpt ? 128 : lo, pos < a.sink || d > tpt ? 128 : d * a.R, c0);
+        } else {                              // columns: keys
+          const int32_t k0 = win_key0(it.w, t);
+          if (t < it.w.ns) {
+            vis = range_bits(0, it.w.s_end - k0, c0);
+          } else {
+            vis = range_bits(max(pos - win + 1 - k0, 0), min(pos - k0 + 1, 128), c0) |
+                  range_bits(0, (int32_t)min64(min64(a.sink - k0, pos - k0 + 1), 128), c0);
+          }
+        }
+        const bool full = __all_sync(0xffffffffu, vis == ~0ull);
+        const float* m = reinterpret_cast<const float*>(base + kWbOffMeta + (int)(n & 1) * 1024) +
+                         c0;
+        if (!W(XB_S_FULL, n)) { ok = false; break; }
+        if (!W(XB_META_FULL + (int)(n & 1), n >> 1)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t s[64];
+        tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(s));
+        tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+        tmem_ld_wait();
+        const uint64_t nl2 = pack_f32x2(__float_as_uint(nl), __float_as_uint(nl));
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {        // columns c0 + 4 q .. + 3
+          uint64_t l0 = nl2, l1 = nl2;
+          if (it.dkv) {
+            const ulonglong2 v = reinterpret_cast<const ulonglong2*>(m)[q];
+            l0 = v.x;
+            l1 = v.y;
+          }
+          float u, v;
+          unpack_f32x2(fma_f32x2(pack_f32x2(s[4 * q], s[4 * q + 1]), scale2, l0), u, v);
+          s[4 * q] = __float_as_uint(ex2_approx(u));
+          s[4 * q + 1] = __float_as_uint(ex2_approx(v));
+          unpack_f32x2(fma_f32x2(pack_f32x2(s[4 * q + 2], s[4 * q + 3]), scale2, l1), u, v);
+          s[4 * q + 2] = __float_as_uint(ex2_approx(u));
+          s[4 * q + 3] = __float_as_uint(ex2_approx(v));
+        }
+        if (!full) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!((vis >> c) & 1)) s[c] = 0u;
+        }
+        if (it.dkv) {
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              pk[q] = pack_bf16x2(u2f(s[32 * cc + 2 * q]), u2f(s[32 * cc + 2 * q + 1]));
+            tmem_st_32x32b_x16(ts + 16 * cc, pk);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(bar + XB_P_FULL);
+        if (!W(XB_DP_FULL, n)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t nd2 = pack_f32x2(__float_as_uint(nd), __float_as_uint(nd));
+        uint32_t pk[32];
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          uint32_t d[32];
+          tmem_ld_32x32b_x32(ts + 128 + 32 * cc, d);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint64_t d0 = nd2, d1 = nd2;
+            if (it.dkv) {
+              const ulonglong2 v = reinterpret_cast<const ulonglong2*>(m + 128)[8 * cc + q];
+              d0 = v.x;
+              d1 = v.y;
+            }
+            const int c = 32 * cc + 4 * q;
+            float u, v;
+            unpack_f32x2(mul_f32x2(pack_f32x2(s[c], s[c + 1]),
+                                   add_f32x2(pack_f32x2(d[4 * q], d[4 * q + 1]), d0)), u, v);
+            if (!full) {                      // dO.v may be anything where nothing is seen
+              u = (vis >> c) & 1 ? u : 0.f;
+              v = (vis >> (c + 1)) & 1 ? v : 0.f;
+            }
+            pk[16 * cc + 2 * q] = pack_bf16x2(u, v);
+            unpack_f32x2(mul_f32x2(pack_f32x2(s[c + 2], s[c + 3]),
+                                   add_f32x2(pack_f32x2(d[4 * q + 2], d[4 * q + 3]), d1)), u, v);
+            if (!full) {
+              u = (vis >> (c + 2)) & 1 ? u : 0.f;
+              v = (vis >> (c + 3)) & 1 ? v : 0.f;
+            }
+            pk[16 * cc + 2 * q + 1] = pack_bf16x2(u, v);
+          }
+        }
+        tmem_st_32x32b_x16(ts + 128, *reinterpret_cast<uint32_t(*)[16]>(pk));
+        tmem_st_32x32b_x16(ts + 144, *reinterpret_cast<uint32_t(*)[16]>(pk + 16));
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar + XB_DS_FULL);
+      }
+      if (!ok) break;
+      // outputs: dk, dv items: warps 0-3 dV, 4-7 dK, a row of 128 each; dq: 64 columns each
+      const bool any = it.nt > 0;
+      if (any) {
+        if (!W(XB_ACC_FULL, ni)) { ok = false; break; }
+        tc_fence_after();
+      }
+      const int ncol = it.dkv ? 4 : 2;        // groups of 32 columns
+      const uint32_t src =
+          tmem + lane_base + (it.dkv ? 256 + 128 * half : 384 + c0);
+      const float f = it.dkv && half == 0 ? 1.f : a.scale;
+      const bool live = any && (it.dkv ? pos < it.len : row_live);
+      const bool store = it.dkv ? pos < a.n_kv : i_row < a.n_q;
+      __nv_bfloat16* dst =
+          it.dkv ? (half == 0 ? a.dv : a.dk) +
+                       (((int64_t)it.b * a.G + it.g) * a.n_kv + pos) * kHeadDim
+                 : a.dq + qrow * kHeadDim + c0;
+      float* pdst = it.dkv && it.part >= 0
+                        ? p.part + (((int64_t)it.part * 2 + half) * 128 + row) * kHeadDim
+                        : nullptr;
+#pragma unroll 1
+      for (int cc = 0; cc < ncol; ++cc) {
+        uint32_t r[32];
+        if (any) {
+          tmem_ld_32x32b_x32(src + 32 * cc, r);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int q = 0; q < 32; ++q) r[q] = live ? __float_as_uint(f * u2f(r[q])) : 0u;
+        if (pdst != nullptr) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            st_global_v8(pdst + 32 * cc + 8 * q, u2f(r[8 * q]), u2f(r[8 * q + 1]),
+                         u2f(r[8 * q + 2]), u2f(r[8 * q + 3]), u2f(r[8 * q + 4]),
+                         u2f(r[8 * q + 5]), u2f(r[8 * q + 6]), u2f(r[8 * q + 7]));
+        } else if (store) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              pk[q] = pack_bf16x2(u2f(r[16 * h + 2 * q]), u2f(r[16 * h + 2 * q + 1]));
+            st_global_v8(reinterpret_cast<float*>(dst + 32 * cc + 16 * h), u2f(pk[0]), u2f(pk[1]),
+                         u2f(pk[2]), u2f(pk[3]), u2f(pk[4]), u2f(pk[5]), u2f(pk[6]), u2f(pk[7]));
+          }
+        }
+      }
+      if (any) {
+        tc_fence_before();
+        mbar_arrive(bar + XB_ACC_EMPTY);
+        ++ni;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// dv, dk of the cut blocks: their chunks' sums added in chunk order.  One block
+// per (batch, group, key block of the cut ones' range).
+__global__ void __launch_bounds__(256)
+    window_bwd_join_kernel(const __grid_constant__ WindowBwdArgs p, int32_t c_lo, int32_t n_c) {
+  const WindowArgs& a = p.w;
+  const int32_t bg = blockIdx.x / n_c, c = c_lo + blockIdx.x - bg * n_c;
+  int32_t first, count;
+  wb_query_tiles(a, c, first, count);
+  const int32_t k = wb_chunks(count, p.chunk);
+  if (k == 1) return;
+  const float4* src = reinterpret_cast<const float4*>(p.part) +
+                      ((int64_t)bg * p.n_part + __ldg(p.pbase + c)) * 8192;
+  for (int i = threadIdx.x; i < 8192; i += 256) {
+    float4 t = __ldg(src + i);
+#pragma unroll 4
+    for (int32_t j = 1; j < k; ++j) {
+      const float4 u = __ldg(src + (int64_t)j * 8192 + i);
+      t.x += u.x;
+      t.y += u.y;
+      t.z += u.z;
+      t.w += u.w;
+    }
+    const int64_t key = (int64_t)c * 128 + ((i >> 5) & 127);
+    if (key >= a.n_kv) continue;
+    __nv_bfloat16* dst = (i >= 4096 ? a.dk : a.dv) +
+                         ((int64_t)bg * a.n_kv + key) * kHeadDim + 4 * (i & 31);
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+  }
+}
+
+size_t window_attn_bwd_workspace(const WindowArgs& a) {
+  const WbPlan p = wb_plan(a);
+  if (p.n_dkv + p.n_dq > 0x7FFFFF00) return 0;
+  return pad32((size_t)a.batch * a.n_q * a.G * a.R * 4) + pad32((size_t)p.n_cut * 8) +
+         pad32((size_t)p.nblk * 4) + 32 +
+         (size_t)a.batch * a.G * p.n_part * 2 * 128 * 128 * sizeof(float);
+}
+
+cudaError_t launch_window_attn_bwd(const CUtensorMap& tm_q, const CUtensorMap& tm_do,
+                                   const CUtensorMap& tm_k, const CUtensorMap& tm_v, WindowArgs a,
+                                   void* ws, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return e;
+  if ((e = cudaFuncSetAttribute(window_attn_bwd_kernel,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kWbSmemBytes)) !=
+      cudaSuccess)
+    return e;
+  cudaFuncAttributes attr;
+  if ((e = cudaFuncGetAttributes(&attr, window_attn_bwd_kernel)) != cudaSuccess) return e;
+  if (attr.numRegs != kWbRegsAtLaunch) return cudaErrorInvalidConfiguration;
+  const WbPlan pl = wb_plan(a);
+  WindowBwdArgs p;
+  p.w = a;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  float* delta = reinterpret_cast<float*>(w);
+  w += pad32((size_t)a.batch * a.n_q * a.G * a.R * 4);
+  int2* table = reinterpret_cast<int2*>(w);
+  w += pad32((size_t)pl.n_cut * 8);
+  int32_t* pbase = reinterpret_cast<int32_t*>(w);
+  w += pad32((size_t)pl.nblk * 4);
+  p.counter = reinterpret_cast<int32_t*>(w);
+  p.part = reinterpret_cast<float*>(w + 32);
+  p.delta = delta;
+  p.table = table;
+  p.pbase = pbase;
+  p.chunk = pl.chunk;
+  p.nblk = (int32_t)pl.nblk;
+  p.n_cut = (int32_t)pl.n_cut;
+  p.n_part = (int32_t)pl.n_part;
+  p.n_dkv = (int32_t)pl.n_dkv;
+  p.n_all = (int32_t)(pl.n_dkv + pl.n_dq);
+  const int64_t rows = a.batch * a.n_q * a.G * a.R;
+  window_bwd_prep_kernel<<<(unsigned)((rows + 7) / 8 + 1), 256, 0, st>>>(
+      a, delta, table, pbase, p.counter, pl.chunk, p.nblk);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  window_attn_bwd_kernel<<<(unsigned)min64(p.n_all, sms), kWbThreads, kWbSmemBytes, st>>>(
+      tm_q, tm_do, tm_k, tm_v, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (pl.n_part > 0) {
+    const int32_t n_c = (int32_t)(pl.c_hi - pl.c_lo);
+    window_bwd_join_kernel<<<(unsigned)(a.batch * a.G * n_c), 256, 0, st>>>(p, (int32_t)pl.c_lo,
+                                                                            n_c);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace msa

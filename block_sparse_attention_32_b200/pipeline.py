@@ -11,8 +11,12 @@ and returns the bf16 output and the fp32 log-sum-exp.  Beside it:
 alignment target, optionally the full causal lse), ``token_select_attention``
 (token-level selection at the same key budget), ``backward`` with ``Grads``
 (dq, dk, dv for an upstream gradient) and ``HostPipeline`` (host buffers,
-copies overlapped).  Every step runs in the library's kernels; this module
-only marshals arguments.
+copies overlapped).  Around the path: ``NormRope`` with ``norm_rope`` /
+``norm_rope_backward`` / ``norm_rope_append`` (per-head norms and rotation of
+queries and keys, dense or into a ``PagedCache``), ``paged_decode`` (one new token
+over the paged cache) and ``window_forward`` / ``window_backward`` (sliding-window
+or full causal attention).  Every step runs in the library's kernels; this
+module only marshals arguments.
 """
 from __future__ import annotations
 
@@ -266,3 +270,227 @@ def check_device_errors(buf: Buffers):
     code = int(buf.dev_err[0].item())
     if code:
         raise capi.MSAError("device", 0) from RuntimeError(capi.DEVERR.get(code, code))
+
+
+# ---------------------------------------------------------------------------
+# around the sparse path: norms + rotation, the paged cache, window attention
+# ---------------------------------------------------------------------------
+def rope_table(n_pos, rot, theta=1.0e6, device="cuda"):
+    """The rotation table [n_pos, rot] fp32 of angles p * theta^(-2 i / rot): rot / 2
+    cosines, then rot / 2 sines; the angles in 64 bits, so far positions keep
+    their precision.  Any other table of this layout (scaled angles) serves too."""
+    inv = float(theta) ** (-torch.arange(0, rot, 2, device=device, dtype=torch.float64) / rot)
+    ang = torch.arange(n_pos, device=device, dtype=torch.float64)[:, None] * inv
+    return torch.cat([ang.cos(), ang.sin()], dim=1).to(torch.float32)
+
+
+@dataclasses.dataclass
+class NormRope:
+    """What a layer keeps for its per-head norms and rotation: the table (None: no
+    rotation), the norm weights fp32 [d] (None: ones), eps and the pairing."""
+    table: torch.Tensor | None
+    w_q: torch.Tensor | None = None
+    w_k: torch.Tensor | None = None
+    eps: float = 1e-6
+    interleaved: bool = False
+
+
+def norm_rope(plan: NormRope, q, k, q_out=None, k_out=None, positions=None, pos0=0,
+              dev_err=None):
+    """Normed and rotated queries [B,T,Hq,D] and keys; q [B,T,Hq,D], k [B,T,Hk,D] bf16
+    (either may be None), D 64 or 128.  Returns (q_out, k_out [B,Hk,T,D], the
+    attention's layout), allocated when not given."""
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if k is not None and k_out is None:
+        k_out = torch.empty((k.shape[0], k.shape[2], k.shape[1], k.shape[3]), dtype=k.dtype,
+                            device=k.device)
+    capi.msa_qk_norm_rope(q, k, plan.w_q, plan.w_k, plan.table, q_out, k_out, positions, pos0,
+                          plan.eps, plan.interleaved, dev_err)
+    return q_out, k_out
+
+
+@dataclasses.dataclass
+class NormRopeGrads:
+    dx_q: torch.Tensor | None
+    dx_k: torch.Tensor | None
+    dw_q: torch.Tensor | None
+    dw_k: torch.Tensor | None
+    ws: torch.Tensor
+
+    @staticmethod
+    def allocate(q, k) -> "NormRopeGrads":
+        some = q if q is not None else k
+        d, dev = some.shape[3], some.device
+        n = capi.msa_qk_norm_rope_bwd_workspace(d)
+
+        def like(t):
+            return None if t is None else torch.empty(t.shape, dtype=torch.bfloat16, device=dev)
+
+        def row(t):
+            return None if t is None else torch.empty((d,), dtype=torch.float32, device=dev)
+
+        return NormRopeGrads(like(q), like(k), row(q), row(k),
+                             torch.empty((n // 4,), dtype=torch.float32, device=dev))
+
+
+def norm_rope_backward(plan: NormRope, q, k, d_q, d_k, grads: NormRopeGrads, positions=None,
+                       pos0=0, dev_err=None):
+    """Gradients of norm_rope for d_q [B,T,Hq,D] and d_k [B,Hk,T,D] (bf16, or fp32 as
+    ``backward`` gives them).  Returns (dx_q, dx_k, dw_q, dw_k)."""
+    capi.msa_qk_norm_rope_bwd(q, k, plan.w_q, plan.w_k, plan.table, d_q, d_k, grads.dx_q,
+                              grads.dx_k, grads.dw_q, grads.dw_k, grads.ws, positions, pos0,
+                              plan.eps, plan.interleaved, dev_err)
+    return grads.dx_q, grads.dx_k, grads.dw_q, grads.dw_k
+
+
+@dataclasses.dataclass
+class PagedCache:
+    """A paged key-value cache: pages seen as [n_pages, h_kv, page_size, 128] (heads
+    or tokens stored outermost), the block table [B, pages per sequence] int32 and
+    the sequences' lengths [B] int32.  Who calls keeps the table and the lengths."""
+    k_pages: torch.Tensor
+    v_pages: torch.Tensor
+    block_table: torch.Tensor
+    seq_lens: torch.Tensor
+
+    @staticmethod
+    def allocate(batch, max_tokens, h_kv, page_size=64, n_pages=None, tokens_outermost=False,
+                 device="cuda") -> "PagedCache":
+        """An empty cache.  Without n_pages every sequence owns pages for
+        max_tokens, else the table starts out at -1."""
+        dev = torch.device(device)
+        per = (max_tokens + page_size - 1) // page_size
+        own = n_pages is None
+        n = batch * per if own else n_pages
+
+        def pages():
+            if tokens_outermost:
+                t = torch.zeros((n, page_size, h_kv, capi.HEAD_DIM), dtype=torch.bfloat16,
+                                device=dev)
+                return t.permute(0, 2, 1, 3)
+            return torch.zeros((n, h_kv, page_size, capi.HEAD_DIM), dtype=torch.bfloat16,
+                               device=dev)
+
+        table = (torch.arange(n, dtype=torch.int32, device=dev).view(batch, per) if own else
+                 torch.full((batch, per), -1, dtype=torch.int32, device=dev))
+        return PagedCache(pages(), pages(), table,
+                          torch.zeros((batch,), dtype=torch.int32, device=dev))
+
+    @property
+    def batch(self):
+        return self.block_table.shape[0]
+
+    @property
+    def h_kv(self):
+        return self.k_pages.shape[1]
+
+    @property
+    def capacity(self):
+        """Tokens a sequence's table row can hold."""
+        return self.block_table.shape[1] * self.k_pages.shape[2]
+
+    def desc(self) -> capi.PagedKV:
+        return capi.paged_kv(self.k_pages, self.v_pages, self.block_table, self.seq_lens)
+
+
+def norm_rope_append(plan: NormRope, q, k, v, positions, q_out, cache: PagedCache, pos0=0,
+                     dev_err=None):
+    """norm_rope whose keys, and the values v [B,T,Hk,128], go into the cache's pages
+    at positions [B, T] int64 (negative: padding; None: pos0 + i).  The table must
+    already map them; seq_lens is the caller's to advance.  Returns q_out."""
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    capi.msa_qk_norm_rope_paged(q, k, v, plan.w_q, plan.w_k, plan.table, q_out, cache.desc(),
+                                cache.batch, positions, pos0, plan.eps, plan.interleaved,
+                                dev_err)
+    return q_out
+
+
+@dataclasses.dataclass
+class DecodeBuffers:
+    dims: capi.Dims
+    out: torch.Tensor
+    lse: torch.Tensor
+    ws: torch.Tensor
+    dev_err: torch.Tensor
+
+    @staticmethod
+    def allocate(cache: PagedCache, h_q, scale=None) -> "DecodeBuffers":
+        dev, B = cache.k_pages.device, cache.batch
+        cap = max(cache.capacity, 1)
+        d = capi.make_dims(B, 1, cap, cap - 1, h_q, cache.h_kv, capi.HEAD_DIM, scale=scale)
+        n = capi.msa_paged_decode_attn_workspace(d)
+        return DecodeBuffers(
+            dims=d,
+            out=torch.empty((B, 1, h_q, capi.HEAD_DIM), dtype=torch.bfloat16, device=dev),
+            lse=torch.empty((B, 1, h_q), dtype=torch.float32, device=dev),
+            ws=torch.empty(((n + 15) // 16 * 4,), dtype=torch.int32, device=dev),
+            dev_err=torch.zeros((4,), dtype=torch.int32, device=dev))
+
+
+def paged_decode(buf: DecodeBuffers, q, cache: PagedCache, window=0, n_sink=0):
+    """Attention of each sequence's newest token (token seq_lens[b] - 1, already in
+    the cache) over its pages: all of them, or a window and sinks.  q [B,1,H,128].
+    Returns (out bf16 [B,1,H,128], lse fp32 [B,1,H]); an empty sequence gives 0, -inf."""
+    capi.msa_paged_decode_attn(buf.dims, q, cache.desc(), cache.batch, buf.out, buf.lse, buf.ws,
+                               window, n_sink, buf.dev_err)
+    return buf.out, buf.lse
+
+
+def window_dims(batch, n_q, n_kv, q_pos0, h_q, h_kv, scale=None) -> capi.Dims:
+    """Dims of a window-attention problem (there is no index branch)."""
+    return capi.make_dims(batch, n_q, n_kv, q_pos0, h_q, h_kv, capi.HEAD_DIM, scale=scale)
+
+
+@dataclasses.dataclass
+class WindowBuffers:
+    dims: capi.Dims
+    window: int
+    n_sink: int
+    out: torch.Tensor
+    lse: torch.Tensor
+    dev_err: torch.Tensor
+    dq: torch.Tensor | None = None
+    dk: torch.Tensor | None = None
+    dv: torch.Tensor | None = None
+    ws: torch.Tensor | None = None
+
+    @staticmethod
+    def allocate(d: capi.Dims, window=0, n_sink=0, backward=False,
+                 device="cuda") -> "WindowBuffers":
+        """Outputs (and, with backward=True, gradients and workspace) of one
+        problem; window 0 is full causal attention."""
+        dev = torch.device(device)
+        qs = (d.batch, d.n_q, d.h_q, capi.HEAD_DIM)
+        ks = (d.batch, d.h_kv, d.n_kv, capi.HEAD_DIM)
+        buf = WindowBuffers(d, window, n_sink,
+                            torch.empty(qs, dtype=torch.bfloat16, device=dev),
+                            torch.empty(qs[:3], dtype=torch.float32, device=dev),
+                            torch.zeros((4,), dtype=torch.int32, device=dev))
+        if backward:
+            n = capi.msa_window_attn_bwd_workspace(d, window, n_sink)
+            buf.dq = torch.empty(qs, dtype=torch.bfloat16, device=dev)
+            buf.dk = torch.empty(ks, dtype=torch.bfloat16, device=dev)
+            buf.dv = torch.empty(ks, dtype=torch.bfloat16, device=dev)
+            buf.ws = torch.empty(((n + 31) // 32 * 8,), dtype=torch.int32, device=dev)
+        return buf
+
+
+def window_forward(buf: WindowBuffers, q, k, v, kv_len=None):
+    """Sliding-window attention with sinks over q [B,n_q,H,128], k, v [B,G,n_kv,128];
+    kv_len int32 [B]: queries at positions >= kv_len[b] are padding (0, -inf).
+    Returns (out, lse)."""
+    capi.msa_window_attn_fwd(buf.dims, buf.window, buf.n_sink, q, k, v, buf.out, buf.lse, kv_len,
+                             buf.dev_err)
+    return buf.out, buf.lse
+
+
+def window_backward(buf: WindowBuffers, q, k, v, d_out, kv_len=None):
+    """Gradients for upstream d_out (bf16) after window_forward on the same buffers.
+    Returns (dq, dk, dv) in bf16."""
+    if buf.ws is None:
+        raise ValueError("allocate the WindowBuffers with backward=True")
+    capi.msa_window_attn_bwd(buf.dims, buf.window, buf.n_sink, q, k, v, buf.out, d_out, buf.lse,
+                             buf.dq, buf.dk, buf.dv, buf.ws, kv_len, buf.dev_err)
+    return buf.dq, buf.dk, buf.dv

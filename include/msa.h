@@ -75,6 +75,9 @@ typedef enum {
 #define MSA_DEVERR_TIMEOUT 1      /* a bounded wait on a barrier ran out */
 #define MSA_DEVERR_BAD_BLOCK 2    /* a selected block id outside [0, own] */
 #define MSA_DEVERR_BAD_ENTRY 3    /* a block->query entry or entry position out of range */
+#define MSA_DEVERR_BAD_POSITION 4 /* a token position past the rotation table */
+#define MSA_DEVERR_BAD_PAGE 5     /* a block-table entry outside the cache's pages */
+#define MSA_DEVERR_BAD_LENGTH 6   /* a sequence length outside its range */
 
 /* Problem sizes.  Query i of batch b sits at absolute position
  * t = q_pos0 + i and may attend keys j <= t; keys are 0 .. n_kv-1 and
@@ -389,6 +392,156 @@ MSA_API msa_status msa_token_select_attention(const msa_dims* dims, msa_tensor q
                                               int64_t budget, int32_t* tokens, float* out,
                                               float* lse, void* ws, size_t ws_bytes,
                                               int32_t* dev_err, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators around the sparse path: what a model needs between its projections
+ * and the attention, in the layers that keep every key or a window of them, and
+ * in a server that keeps its keys and values in pages.  The pages describe the
+ * sparse layers only (their inputs stand for rotated queries and keys); the
+ * definitions here are the textbook ones, written out at each entry point.
+ * ------------------------------------------------------------------------- */
+
+/* Sizes of the per-head norm + rotation.  h_q or h_k may be 0 (that tensor is
+ * not touched and may be null), not both.  d in {64, 128}: the main heads and
+ * both widths of the index branch.  rot: the leading features that turn, a
+ * multiple of 16 in [0, d].  interleaved 0 pairs features (i, i + rot / 2), 1
+ * pairs (2 i, 2 i + 1).  Token i of batch b is at position positions[b, i], or
+ * pos0 + i without positions. */
+typedef struct {
+  int64_t batch, n_tok, pos0;
+  int32_t h_q, h_k, d, rot, interleaved;
+  float eps;
+} msa_norm_rope_dims;
+
+/* Per-head RMS norm and rotary position embedding in one pass.  For a head
+ * vector x, weights w and the table row of the token's position (cosines
+ * c_0 .. c_{rot/2-1}, then sines s_0 .. s_{rot/2-1}):
+ *   y = w * x / sqrt(mean(x^2) + eps)      (all d features)
+ *   (y_a, y_b) = (y_a c_i - y_b s_i, y_b c_i + y_a s_i)   for pair i
+ * in fp32, rounded to bf16 once.
+ *   q [B, n_tok, h_q, d], k [B, n_tok, h_k, d]  bf16 (msa_tensor strides)
+ *   w_q, w_k  [d] fp32, 16-byte aligned, or NULL (ones)
+ *   table     [n_pos, rot] fp32, 16-byte aligned (may be NULL with rot = 0)
+ *   positions [B, n_tok] int64, or NULL.  A negative position marks padding:
+ *             the token's outputs are left as they were.  One >= n_pos sets
+ *             MSA_DEVERR_BAD_POSITION and is treated the same way.  Without
+ *             positions pos0 + n_tok <= n_pos is required.
+ *   q_out     [B, n_tok, h_q, d], k_out: the same for h_k; any strides, so k_out
+ *             can be the attention's [B, h_k, n, d].  An output may be its input
+ *             itself (same pointer and strides), not overlap it otherwise. */
+MSA_API msa_status msa_qk_norm_rope(const msa_norm_rope_dims* dims, msa_tensor q, msa_tensor k,
+                                    const float* w_q, const float* w_k, const float* table,
+                                    int64_t n_pos, const int64_t* positions, msa_tensor q_out,
+                                    msa_tensor k_out, int32_t* dev_err, void* stream);
+
+/* A paged key-value cache: pages of page_size tokens (a power of two >= 16) of
+ * h_kv heads x 128 bf16 values.  Element strides of the page, token and head
+ * dimensions, the same for K and V (multiples of 8), so a page may hold heads
+ * or tokens outermost.  Token j of sequence b is row j % page_size of page
+ * block_table[b * table_stride + j / page_size].  seq_lens: int32 [batch], the
+ * tokens each sequence has (used by the attention only). */
+typedef struct {
+  void *k, *v;
+  int64_t n_pages, s_page, s_tok, s_head;
+  const int32_t* block_table;
+  int64_t table_stride;
+  const int32_t* seq_lens;
+  int32_t page_size, h_kv;
+} msa_paged_kv;
+
+/* msa_qk_norm_rope whose keys go into a paged cache at their positions, with
+ * the values v [B, n_tok, h_k, 128] (bf16, copied) beside them: d = 128, h_k =
+ * cache->h_kv.  The page of every token written must be in the table before
+ * the call; a table entry outside [0, n_pages), or a position past the table's
+ * row, sets MSA_DEVERR_BAD_PAGE and leaves the cache alone for that token (its
+ * q_out row is written).  Two tokens of one call must not have the same place
+ * in the cache. */
+MSA_API msa_status msa_qk_norm_rope_paged(const msa_norm_rope_dims* dims, msa_tensor q,
+                                          msa_tensor k, msa_tensor v, const float* w_q,
+                                          const float* w_k, const float* table, int64_t n_pos,
+                                          const int64_t* positions, msa_tensor q_out,
+                                          const msa_paged_kv* cache, int32_t* dev_err,
+                                          void* stream);
+
+/* Backward of msa_qk_norm_rope.  With r = 1 / sqrt(mean(x^2) + eps), xh = r x
+ * and dz the upstream gradient turned back by the token's angles:
+ *   dw = sum over batch, tokens and heads of dz * xh
+ *   dx = r (dz w - xh mean(dz w xh))
+ *   d_q, d_k    gradients of q_out, k_out: bf16, or fp32 (as the sparse
+ *               backward gives them) when dy_fp32 is 1; msa_tensor strides in
+ *               elements
+ *   dx_q, dx_k  bf16, the shape of q and k; rows of tokens at a negative (or
+ *               bad) position are left as they were and add nothing to dw
+ *   dw_q, dw_k  [d] fp32, or NULL
+ *   ws          msa_qk_norm_rope_bwd_workspace() bytes, 16-byte aligned */
+MSA_API size_t msa_qk_norm_rope_bwd_workspace(const msa_norm_rope_dims* dims);
+MSA_API msa_status msa_qk_norm_rope_bwd(const msa_norm_rope_dims* dims, msa_tensor q,
+                                        msa_tensor k, const float* w_q, const float* w_k,
+                                        const float* table, int64_t n_pos,
+                                        const int64_t* positions, msa_tensor d_q, msa_tensor d_k,
+                                        int32_t dy_fp32, msa_tensor dx_q, msa_tensor dx_k,
+                                        float* dw_q, float* dw_k, void* ws, size_t ws_bytes,
+                                        int32_t* dev_err, void* stream);
+
+/* Attention of one new token per sequence over a paged cache, split over the
+ * cache's length and joined.  dims: n_q = 1, n_kv = the most tokens a sequence
+ * may have (<= table_stride * page_size), h_kv = cache->h_kv; q_pos0, h_kidx,
+ * d_idx and q_window have no meaning here (any valid values).  With L =
+ * seq_lens[b] (read on the device; the new token is token L - 1, already in the
+ * cache) and J = {j < L : window = 0 or L - 1 - j < window or j < n_sink}:
+ *   out[b, 0, h] = sum_{j in J} softmax_{j in J}(scale q_h.k_j) v_j
+ *   lse[b, 0, h] = ln sum_{j in J} e^{scale q_h.k_j}
+ *   q [B, 1, h_q, 128] bf16 (msa_tensor strides); out [B, 1, h_q, 128] bf16 and
+ *   lse [B, 1, h_q] fp32 contiguous; L = 0 gives out = 0, lse = -inf.
+ * A length outside [0, n_kv] sets MSA_DEVERR_BAD_LENGTH and is clamped.  A
+ * table entry outside [0, n_pages) under a visible token sets
+ * MSA_DEVERR_BAD_PAGE, and the page's tokens count as not visible; pages with no
+ * visible token are not read and their entries may be anything.  What the cache
+ * holds at tokens that are not visible has no influence.
+ *   ws  msa_paged_decode_attn_workspace() bytes, 16-byte aligned; contents on
+ *       entry do not matter.  Calls that overlap on the GPU need a ws each.
+ * batch <= 4096, window and n_sink >= 0. */
+MSA_API size_t msa_paged_decode_attn_workspace(const msa_dims* dims);
+MSA_API msa_status msa_paged_decode_attn(const msa_dims* dims, int64_t window, int64_t n_sink,
+                                         msa_tensor q, const msa_paged_kv* cache, void* out,
+                                         float* lse, void* ws, size_t ws_bytes, int32_t* dev_err,
+                                         void* stream);
+
+/* Attention with a sliding window and sink tokens: query i of batch b, at
+ * position t = q_pos0 + i, sees J(t) = {j <= t : window = 0 or t - j < window or
+ * j < n_sink} (window 0: full causal attention):
+ *   out = sum_{j in J} softmax_{j in J}(scale q.k_j) v_j,  lse = ln sum e^{scale q.k_j}.
+ *   q [B, n_q, h_q, 128], k, v [B, h_kv, n_kv, 128] bf16 (msa_tensor strides)
+ *   kv_len [B] int32 (device) or NULL: queries at t >= kv_len[b] are padding,
+ *          out = 0 and lse = -inf; what q, k and v hold from kv_len[b] on has no
+ *          influence on the others.  A value outside [0, n_kv] sets
+ *          MSA_DEVERR_BAD_LENGTH and is clamped.
+ *   out [B, n_q, h_q, 128] bf16 (32-byte aligned), lse [B, n_q, h_q] fp32,
+ *   contiguous.  d_idx, h_kidx and q_window of dims have no meaning here.
+ * K and V must be finite at the keys below kv_len. */
+MSA_API msa_status msa_window_attn_fwd(const msa_dims* dims, int64_t window, int64_t n_sink,
+                                       msa_tensor q, msa_tensor k, msa_tensor v,
+                                       const int32_t* kv_len, void* out, float* lse,
+                                       int32_t* dev_err, void* stream);
+
+/* Backward of msa_window_attn_fwd.  With p_j = e^{scale q.k_j - lse} over J(t),
+ * D = dO.o and dS_j = p_j (dO.v_j - D):
+ *   dq = scale sum_j dS_j k_j,  dk_j = scale sum dS_j q,  dv_j = sum p_j dO,
+ * the last two over every (query, head of the group) that sees j.
+ *   o, lse       the forward's results; d_o [B, n_q, h_q, 128] bf16
+ *   dq           [B, n_q, h_q, 128] bf16, contiguous, 32-byte aligned
+ *   dk, dv       [B, h_kv, n_kv, 128] bf16, contiguous, 32-byte aligned
+ *   ws           msa_window_attn_bwd_workspace() bytes, 32-byte aligned
+ * All three are summed in fp32 and rounded to bf16 once; padded queries get
+ * dq = 0 and add nothing, keys that nobody sees get 0.  Bit-identical from run to
+ * run. */
+MSA_API size_t msa_window_attn_bwd_workspace(const msa_dims* dims, int64_t window,
+                                             int64_t n_sink);
+MSA_API msa_status msa_window_attn_bwd(const msa_dims* dims, int64_t window, int64_t n_sink,
+                                       msa_tensor q, msa_tensor k, msa_tensor v, msa_tensor o,
+                                       msa_tensor d_o, const float* lse, const int32_t* kv_len,
+                                       void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                                       int32_t* dev_err, void* stream);
 
 /* Debug setting (the pages have no counterpart): the time limit, in
  * nanoseconds, of every barrier wait inside the kernels that
