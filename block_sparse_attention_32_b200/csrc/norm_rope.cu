@@ -10,13 +10,15 @@
 //   dw = sum over rows dz * xh,   dx = (dz w - xh mean(dz w xh)) / sqrt(...).
 //
 // Bound: HBM -- every value is read once and written once (2 + 2 bytes per
-// feature forward).  A row lives in D / 8 lanes, 16 bytes each, so one load, a
-// few shuffles (sum of squares; the partner feature, which for pairs (i, i +
-// rot / 2) is always whole lanes away because rot is a multiple of 16) and
-// one store do the work in registers.  The D / 8 lanes keep one token and walk
-// `hc` of its heads: the token's cosines and sines (fp32, the size of two bf16
-// rows) are read once per hc heads, kept in registers.  Everything is computed
-// in fp32 and rounded to bf16 once, at the store.
+// feature forward, 2 + 2 or 4 + 2 backward).  A row lives in D / 8 lanes of 8
+// features each.  For pairs (i, i + rot / 2) a lane takes features 4 l .. 4 l + 3 of
+// both halves (two 8-byte loads), so that both partners of every pair are its
+// own and the rotation needs no exchange; the features behind rot go to the
+// lanes left over.  Only the sum of squares (and, backward, one more sum) crosses
+// lanes.  The D / 8 lanes keep one token and walk `hc` of its heads: the token's
+// cosines and sines (fp32, the size of two bf16 rows) are read once per hc heads
+// and kept in registers.  Everything is computed in fp32 and rounded to bf16 once,
+// at the store.
 #include "common.cuh"
 #include "layer_args.cuh"
 
@@ -35,56 +37,78 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 
-// cosines and sines of the lane's 8 features: pairs (i, i + rot / 2): one per
-// feature; adjacent pairs: entries 0..3, one per pair.  Lanes past rot keep 1, 0.
+// offsets of a lane's two runs of 4 features; `turns`: they are rotated
+struct LanePos {
+  int o0, o1, ang;     // ang: first of its 4 angles
+  bool turns;
+};
 template <bool kInter>
-__device__ __forceinline__ void load_angles(const float* __restrict__ row, int rot, int ln,
-                                            float (&c)[8], float (&s)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = 1.f;
-    s[i] = 0.f;
-  }
-  const int half = rot >> 1;
-  if (8 * ln >= rot) return;
+__device__ __forceinline__ LanePos lane_pos(int ln, int rot) {
+  LanePos p;
   if (kInter) {
-    const float4 c0 = __ldg(reinterpret_cast<const float4*>(row + 4 * ln));
-    const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + half + 4 * ln));
-    c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w;
-    s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w;
+    p.o0 = 8 * ln;
+    p.o1 = 8 * ln + 4;
+    p.ang = 4 * ln;
+    p.turns = 8 * ln < rot;
   } else {
-    const int i0 = 8 * ln < half ? 8 * ln : 8 * ln - half;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float4 c0 = __ldg(reinterpret_cast<const float4*>(row + i0) + j);
-      const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + half + i0) + j);
-      c[4 * j] = c0.x; c[4 * j + 1] = c0.y; c[4 * j + 2] = c0.z; c[4 * j + 3] = c0.w;
-      s[4 * j] = s0.x; s[4 * j + 1] = s0.y; s[4 * j + 2] = s0.z; s[4 * j + 3] = s0.w;
-    }
+    const int half = rot >> 1;
+    p.turns = 4 * ln < half;
+    p.ang = 4 * ln;
+    // rot is a multiple of 16, so the lanes behind rot / 8 hold whole runs of 8
+    p.o0 = p.turns ? 4 * ln : 8 * ln;
+    p.o1 = p.turns ? half + 4 * ln : 8 * ln + 4;
+  }
+  return p;
+}
+template <bool kInter>
+__device__ __forceinline__ uint4 load_row(const __nv_bfloat16* p, const LanePos& l) {
+  if (kInter) return *reinterpret_cast<const uint4*>(p + l.o0);
+  const uint2 a = *reinterpret_cast<const uint2*>(p + l.o0);
+  const uint2 b = *reinterpret_cast<const uint2*>(p + l.o1);
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
+template <bool kInter>
+__device__ __forceinline__ void store_row(__nv_bfloat16* p, const LanePos& l, const uint4& v) {
+  if (kInter) {
+    *reinterpret_cast<uint4*>(p + l.o0) = v;
+  } else {
+    *reinterpret_cast<uint2*>(p + l.o0) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(p + l.o1) = make_uint2(v.z, v.w);
   }
 }
 
-// turns y by the angles (sgn 1) or back (sgn -1); every lane of the warp calls it
-template <bool kInter, int kLanes>
-__device__ __forceinline__ void rotate8(float (&y)[8], const float (&c)[8], const float (&s)[8],
-                                        int rot, int ln, float sgn) {
-  if (kInter) {
+// cosines and sines of the lane's 4 pairs (1, 0 where nothing turns)
+__device__ __forceinline__ void load_angles(const float* __restrict__ row, int rot,
+                                            const LanePos& l, bool want, float (&c)[4],
+                                            float (&s)[4]) {
+  float4 cv = make_float4(1.f, 1.f, 1.f, 1.f), sv = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (want && l.turns) {
+    cv = __ldg(reinterpret_cast<const float4*>(row + l.ang));
+    sv = __ldg(reinterpret_cast<const float4*>(row + (rot >> 1) + l.ang));
+  }
+  c[0] = cv.x; c[1] = cv.y; c[2] = cv.z; c[3] = cv.w;
+  s[0] = sv.x; s[1] = sv.y; s[2] = sv.z; s[3] = sv.w;
+}
+__device__ __forceinline__ void load_weights(const float* __restrict__ w, const LanePos& l,
+                                             float (&v)[8]) {
+  float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = a;
+  if (w != nullptr) {
+    a = __ldg(reinterpret_cast<const float4*>(w + l.o0));
+    b = __ldg(reinterpret_cast<const float4*>(w + l.o1));
+  }
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// turns y by the angles (kSign 1) or back (-1)
+template <bool kInter, int kSign>
+__device__ __forceinline__ void rotate8(float (&y)[8], const float (&c)[4], const float (&s)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = y[2 * i], b = y[2 * i + 1], sn = sgn * s[i];
-      y[2 * i] = a * c[i] - b * sn;
-      y[2 * i + 1] = b * c[i] + a * sn;
-    }
-  } else {
-    const int hl = rot >> 4;                       // lanes of one half
-    const bool first = ln < hl;
-    const int peer = 8 * ln < rot ? (first ? ln + hl : ln - hl) : ln;
-    const float f = first ? -sgn : sgn;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_sync(0xffffffffu, y[i], peer, kLanes);
-      y[i] = y[i] * c[i] + f * o * s[i];
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int ia = kInter ? 2 * i : i, ib = kInter ? 2 * i + 1 : i + 4;
+    const float a = y[ia], b = y[ib], sn = kSign > 0 ? s[i] : -s[i];
+    y[ia] = a * c[i] - b * sn;
+    y[ib] = b * c[i] + a * sn;
   }
 }
 
@@ -108,34 +132,43 @@ __device__ __forceinline__ int64_t token_pos(const NormRopeArgs& a, int64_t bt, 
 }
 
 constexpr int kNrThreads = 256;
-constexpr int kNrUnroll = 4;       // rows in flight per lane
+constexpr int kNrHeads = 8;        // heads of a token per item; all loaded before the first is used
 
 template <int kD, bool kInter, bool kPaged>
 __global__ void __launch_bounds__(kNrThreads)
     norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int kLanes = kD / 8;
   const int ln = threadIdx.x % kLanes;
-  const int64_t item = (int64_t)blockIdx.x * (kNrThreads / kLanes) + threadIdx.x / kLanes;
+  const LanePos lp = lane_pos<kInter>(ln, a.rot);
+  const uint32_t item = blockIdx.x * (kNrThreads / kLanes) + threadIdx.x / kLanes;
   const bool in = item < a.n_items;                 // lanes past the end still join the shuffles
-  const int32_t per_tok = a.chunks[0] + a.chunks[1] + a.chunks[2];
-  const int64_t bt = in ? item / per_tok : 0;
+  const uint32_t per_tok = a.chunks[0] + a.chunks[1] + a.chunks[2];
+  const uint32_t bt = in ? item / per_tok : 0;
   int32_t ch = in ? (int32_t)(item - bt * per_tok) : 0;
   int kind = 0;
   if (ch >= a.chunks[0]) {
     ch -= a.chunks[0];
     kind = 1;
-    if (ch >= a.chunks[1]) {
+    if (kPaged && ch >= a.chunks[1]) {
       ch -= a.chunks[1];
       kind = 2;
     }
   }
-  const int64_t b = bt / a.n_tok, i = bt - b * a.n_tok;
+  const uint32_t b = bt / (uint32_t)a.n_tok, i = bt - b * (uint32_t)a.n_tok;
+  const int h0 = ch * a.hc, h1 = min(h0 + a.hc, a.heads[kind]);
+  const __nv_bfloat16* src =
+      a.src[kind] + b * a.ss_b[kind] + i * a.ss_t[kind] + h0 * a.ss_h[kind];
   const int64_t pos = in ? token_pos(a, bt, i) : -1;
   bool live = pos >= 0;
-  const int h0 = ch * a.hc, h1 = min(h0 + a.hc, a.heads[kind]);
+  uint4 v[kNrHeads];
+#pragma unroll
+  for (int u = 0; u < kNrHeads; ++u) {
+    v[u] = make_uint4(0, 0, 0, 0);
+    if (live && h0 + u < h1) v[u] = load_row<kInter>(src + u * a.ss_h[kind], lp);
+  }
   __nv_bfloat16* dst = nullptr;
   if (live) {
-    dst = a.dst[kind] + 8 * ln;
+    dst = a.dst[kind] + h0 * a.ds_h[kind];
     if (kPaged && kind > 0) {
       const int64_t pi = pos / a.page_size;
       const int64_t pg =
@@ -149,55 +182,39 @@ __global__ void __launch_bounds__(kNrThreads)
       dst += b * a.ds_b[kind] + i * a.ds_t[kind];
     }
   }
-  const __nv_bfloat16* src = a.src[kind] + b * a.ss_b[kind] + i * a.ss_t[kind] + 8 * ln;
-  float c[8], s[8], w[8];
+  float c[4], s[4], w[8];
   const bool norm = !kPaged || kind < 2;
-  load_angles<kInter>(a.table + (live ? pos : 0) * a.rot, live && norm ? a.rot : 0, ln, c, s);
+  load_angles(a.table + (live ? pos : 0) * a.rot, a.rot, lp, live && norm, c, s);
+  load_weights(norm ? a.w[kPaged ? min(kind, 1) : kind] : nullptr, lp, w);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = 1.f;
-  if (norm && a.w[kind] != nullptr) {
-    const float4 w0 = __ldg(reinterpret_cast<const float4*>(a.w[kind] + 8 * ln));
-    const float4 w1 = __ldg(reinterpret_cast<const float4*>(a.w[kind] + 8 * ln) + 1);
-    w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
-    w[4] = w1.x; w[5] = w1.y; w[6] = w1.z; w[7] = w1.w;
-  }
-  for (int hb = 0; hb < a.hc; hb += kNrUnroll) {
-    uint4 v[kNrUnroll];
+  for (int u = 0; u < kNrHeads; ++u) {
+    if (u >= a.hc) break;                           // the same for every lane
+    float x[8];
+    unpack8(v[u], x);
+    float ss = 0.f;
 #pragma unroll
-    for (int u = 0; u < kNrUnroll; ++u) {
-      const int h = h0 + hb + u;
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (live && h < h1) v[u] = *reinterpret_cast<const uint4*>(src + h * a.ss_h[kind]);
-    }
+    for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
+    ss = row_sum<kLanes>(ss);
+    const float r = rsqrtf(ss * (1.f / kD) + a.eps);
 #pragma unroll
-    for (int u = 0; u < kNrUnroll; ++u) {
-      const int h = h0 + hb + u;
-      float x[8];
-      unpack8(v[u], x);
-      float ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
-      ss = row_sum<kLanes>(ss);
-      const float r = rsqrtf(ss * (1.f / kD) + a.eps);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
-      rotate8<kInter, kLanes>(x, c, s, a.rot, ln, 1.f);
-      if (live && h < h1)
-        *reinterpret_cast<uint4*>(dst + h * a.ds_h[kind]) = norm ? pack8(x) : v[u];
-    }
+    for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
+    rotate8<kInter, 1>(x, c, s);
+    if (live && h0 + u < h1) store_row<kInter>(dst + u * a.ds_h[kind], lp, norm ? pack8(x) : v[u]);
   }
 }
 
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-template <bool kF32>
-__device__ __forceinline__ void load_dy(const void* p, int64_t off, uint4 (&v)[2]) {
+template <bool kInter, bool kF32>
+__device__ __forceinline__ void load_dy(const void* p, int64_t off, const LanePos& l,
+                                        uint4 (&v)[2]) {
   if (kF32) {
-    v[0] = *reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p) + off);
-    v[1] = *reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p) + off + 4);
+    const float* y = reinterpret_cast<const float*>(p) + off;
+    v[0] = *reinterpret_cast<const uint4*>(y + l.o0);
+    v[1] = *reinterpret_cast<const uint4*>(y + l.o1);
   } else {
-    v[0] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p) + off);
+    v[0] = load_row<kInter>(reinterpret_cast<const __nv_bfloat16*>(p) + off, l);
   }
 }
 template <bool kF32>
@@ -213,51 +230,57 @@ __device__ __forceinline__ void unpack_dy(const uint4 (&v)[2], float (&y)[8]) {
   }
 }
 
-// Persistent blocks: the lanes of a row keep their 8 features' weight-gradient
-// sums in fp32 registers over all the rows they meet, then the block's rows
-// are added in a fixed order and leave as one partial row; a second kernel adds
-// the blocks in a fixed order.  No atomics: the same bits every run.
+// Persistent blocks over the items, all of the queries' before the keys': the
+// lanes of a row keep their 8 features' weight-gradient sums in fp32 registers
+// over all the rows they meet, then the block's rows are added in a fixed order
+// and leave as one partial row; a second kernel adds the blocks in a fixed
+// order.  No atomics: the same bits every run.
+constexpr int kNrBwdUnroll = 4;    // rows in flight per lane
+
 template <int kD, bool kInter, bool kF32>
-__global__ void __launch_bounds__(kNrThreads)
+__global__ void __launch_bounds__(kNrThreads, 2)
     norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdArgs p) {
-  constexpr int kLanes = kD / 8, kGroups = kNrThreads / kLanes, kU = 2;
+  constexpr int kLanes = kD / 8, kGroups = kNrThreads / kLanes, kU = kNrBwdUnroll;
   const NormRopeArgs& a = p.f;
   __shared__ float red[kGroups][kD + 4];
   const int ln = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-  const int32_t per_tok = a.chunks[0] + a.chunks[1];
-  float dw[2][8];
+  const LanePos lp = lane_pos<kInter>(ln, a.rot);
+  float dwq[8], g[8], w[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) dw[0][j] = dw[1][j] = 0.f;
-  const int64_t step = (int64_t)gridDim.x * kGroups;
+  for (int j = 0; j < 8; ++j) dwq[j] = g[j] = 0.f;
+  int cur = 0;                                      // kind that g belongs to
+  load_weights(a.w[0], lp, w);
+  const uint32_t n_items = (uint32_t)a.n_items;
+  const uint32_t nq = (uint32_t)(a.batch * a.n_tok) * a.chunks[0];
+  const uint32_t step = gridDim.x * kGroups;
   // every group runs the same number of rounds, so the shuffles stay whole
-  const int64_t rounds = (a.n_items + step - 1) / step;
-  for (int64_t rd = 0; rd < rounds; ++rd) {
-    const int64_t item = rd * step + (int64_t)blockIdx.x * kGroups + grp;
-    const bool in = item < a.n_items;
-    const int64_t bt = in ? item / per_tok : 0;
-    int32_t ch = in ? (int32_t)(item - bt * per_tok) : 0;
-    const int kind = ch >= a.chunks[0] ? 1 : 0;
-    if (kind) ch -= a.chunks[0];
-    const int64_t b = bt / a.n_tok, i = bt - b * a.n_tok;
+  const uint32_t rounds = (n_items + step - 1) / step;
+  for (uint32_t rd = 0; rd < rounds; ++rd) {
+    const uint32_t item = rd * step + blockIdx.x * kGroups + grp;
+    const bool in = item < n_items;
+    const int kind = in && item >= nq ? 1 : 0;
+    const uint32_t it = in ? (kind ? item - nq : item) : 0;
+    const uint32_t per = max(a.chunks[kind], 1);
+    const uint32_t bt = it / per;
+    const int32_t ch = (int32_t)(it - bt * per);
+    const uint32_t b = bt / (uint32_t)a.n_tok, i = bt - b * (uint32_t)a.n_tok;
+    if (in && kind != cur) {
+      cur = kind;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dwq[j] = g[j];
+        g[j] = 0.f;
+      }
+      load_weights(a.w[1], lp, w);
+    }
     const int64_t pos = in ? token_pos(a, bt, i) : -1;
     const bool live = pos >= 0;
     const int h0 = ch * a.hc, h1 = min(h0 + a.hc, a.heads[kind]);
-    const __nv_bfloat16* src = a.src[kind] + b * a.ss_b[kind] + i * a.ss_t[kind] + 8 * ln;
-    __nv_bfloat16* dst = a.dst[kind] + b * a.ds_b[kind] + i * a.ds_t[kind] + 8 * ln;
-    const int64_t yo = b * p.ys_b[kind] + i * p.ys_t[kind] + 8 * ln;
-    float c[8], s[8], w[8];
-    load_angles<kInter>(a.table + (live ? pos : 0) * a.rot, live ? a.rot : 0, ln, c, s);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 1.f;
-    if (a.w[kind] != nullptr) {
-      const float4 w0 = __ldg(reinterpret_cast<const float4*>(a.w[kind] + 8 * ln));
-      const float4 w1 = __ldg(reinterpret_cast<const float4*>(a.w[kind] + 8 * ln) + 1);
-      w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
-      w[4] = w1.x; w[5] = w1.y; w[6] = w1.z; w[7] = w1.w;
-    }
-    float g[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = 0.f;
+    const __nv_bfloat16* src = a.src[kind] + b * a.ss_b[kind] + i * a.ss_t[kind];
+    __nv_bfloat16* dst = a.dst[kind] + b * a.ds_b[kind] + i * a.ds_t[kind];
+    const int64_t yo = b * p.ys_b[kind] + i * p.ys_t[kind];
+    float c[4], s[4];
+    load_angles(a.table + (live ? pos : 0) * a.rot, a.rot, lp, live, c, s);
     for (int hb = 0; hb < a.hc; hb += kU) {
       uint4 xv[kU], yv[kU][2];
 #pragma unroll
@@ -265,17 +288,18 @@ __global__ void __launch_bounds__(kNrThreads)
         const int h = h0 + hb + u;
         xv[u] = yv[u][0] = yv[u][1] = make_uint4(0, 0, 0, 0);
         if (live && h < h1) {
-          xv[u] = *reinterpret_cast<const uint4*>(src + h * a.ss_h[kind]);
-          load_dy<kF32>(p.dy[kind], yo + h * p.ys_h[kind], yv[u]);
+          xv[u] = load_row<kInter>(src + h * a.ss_h[kind], lp);
+          load_dy<kInter, kF32>(p.dy[kind], yo + h * p.ys_h[kind], lp, yv[u]);
         }
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int h = h0 + hb + u;
+        if (hb + u >= a.hc) break;                  // the same for every lane
         float x[8], y[8];
         unpack8(xv[u], x);
         unpack_dy<kF32>(yv[u], y);
-        rotate8<kInter, kLanes>(y, c, s, a.rot, ln, -1.f);
+        rotate8<kInter, -1>(y, c, s);
         float ss = 0.f, sy = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -293,19 +317,17 @@ __global__ void __launch_bounds__(kNrThreads)
           g[j] += y[j] * xh;
           x[j] = r * (y[j] * w[j] - xh * m);
         }
-        if (live && h < h1) *reinterpret_cast<uint4*>(dst + h * a.ds_h[kind]) = pack8(x);
+        if (live && h < h1) store_row<kInter>(dst + h * a.ds_h[kind], lp, pack8(x));
       }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      dw[0][j] += kind ? 0.f : g[j];
-      dw[1][j] += kind ? g[j] : 0.f;
     }
   }
   for (int k = 0; k < 2; ++k) {
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) red[grp][8 * ln + j] = dw[k][j];
+    for (int j = 0; j < 8; ++j) {
+      const float t = k == 0 ? (cur == 0 ? g[j] : dwq[j]) : (cur == 0 ? 0.f : g[j]);
+      red[grp][(j < 4 ? lp.o0 : lp.o1 - 4) + j] = t;
+    }
     __syncthreads();
     if (threadIdx.x < kD) {
       float t = 0.f;
@@ -364,17 +386,16 @@ cudaError_t launch_norm_rope(NormRopeArgs a, int32_t d, bool inter, bool paged,
   const int kinds = paged ? 3 : 2, groups = kNrThreads / (d / 8);
   // eight heads per token's angles when that still fills the GPU; two when it
   // does not, so that a decode step spreads over more SMs
-  split_heads(a, kinds, 8);
+  split_heads(a, kinds, kNrHeads);
   if (a.n_items < (int64_t)148 * 4 * groups) split_heads(a, kinds, 2);
+  if (a.n_items > 0x7FFFFF00) return cudaErrorInvalidValue;
   const int64_t grid = (a.n_items + groups - 1) / groups;
-  if (grid == 0) return cudaSuccess;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   if (d == 128) pick_fwd<128>(a, inter, paged, (unsigned)grid, st);
   else pick_fwd<64>(a, inter, paged, (unsigned)grid, st);
   return cudaGetLastError();
 }
 
-constexpr int kNrBwdBlocks = 148 * 4;     // partial rows at most (the workspace's size)
+constexpr int kNrBwdBlocks = 148 * 2;     // the blocks that fit at once; the workspace's rows
 
 size_t norm_rope_bwd_workspace(int32_t d) { return (size_t)kNrBwdBlocks * 2 * d * sizeof(float); }
 
@@ -394,7 +415,8 @@ cudaError_t launch_norm_rope_bwd(NormRopeBwdArgs p, int32_t d, bool inter, bool 
                                  float* dw_k, cudaStream_t st) {
   const int groups = kNrThreads / (d / 8);
   split_heads(p.f, 2, 8);
-  if (p.f.n_items < (int64_t)kNrBwdBlocks * groups) split_heads(p.f, 2, 2);
+  if (p.f.n_items < (int64_t)kNrBwdBlocks * groups * 4) split_heads(p.f, 2, 2);
+  if (p.f.n_items > 0x7FFFFF00) return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)min64((p.f.n_items + groups - 1) / groups, kNrBwdBlocks);
   if (d == 128) pick_bwd<128>(p, inter, f32, grid, st);
   else pick_bwd<64>(p, inter, f32, grid, st);

@@ -158,30 +158,40 @@ __device__ __forceinline__ uint64_t range_bits(int32_t lo, int32_t hi, int32_t c
 }
 }  // namespace
 
-// D = dO.o of every row, a warp each; the last block lays out the cut key blocks
-// and sets the item counter back
+// D = dO.o of every row: 16 lanes of 16 bytes a row, 4 rows in flight a lane; the
+// last block lays out the cut key blocks and sets the item counter back
+constexpr int kWbPrepRows = 64;        // rows of a 256-thread block
 __global__ void __launch_bounds__(256)
     window_bwd_prep_kernel(const __grid_constant__ WindowArgs a, float* __restrict__ delta,
                            int2* __restrict__ table, int32_t* __restrict__ pbase,
                            int32_t* __restrict__ counter, int32_t chunk, int32_t nblk) {
   const int lane = threadIdx.x & 31;
   if (blockIdx.x + 1 < gridDim.x) {
-    const int64_t H = (int64_t)a.G * a.R;
-    const int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (r >= a.batch * a.n_q * H) return;
-    const int64_t h = r % H, bt = r / H, b = bt / a.n_q, t = bt - b * a.n_q;
-    const uint2 ov = *reinterpret_cast<const uint2*>(a.o + b * a.os_b + t * a.os_t + h * a.os_h +
-                                                     4 * lane);
-    const uint2 dv = *reinterpret_cast<const uint2*>(a.d_o + b * a.ds_b + t * a.ds_t +
-                                                     h * a.ds_h + 4 * lane);
-    const float2 o0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ov.x));
-    const float2 o1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ov.y));
-    const float2 d0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&dv.x));
-    const float2 d1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&dv.y));
-    float s = o0.x * d0.x + o0.y * d0.y + o1.x * d1.x + o1.y * d1.y;
+    const uint32_t H = (uint32_t)(a.G * a.R), n = (uint32_t)a.n_q;
+    const uint32_t rows = (uint32_t)a.batch * n * H;
+    const uint32_t r0 = blockIdx.x * kWbPrepRows + (threadIdx.x >> 4);
+    const int c = 8 * (threadIdx.x & 15);
+    uint4 ov[4], dv[4];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    if (lane == 0) delta[r] = s;
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t r = min(r0 + 16 * u, rows - 1);
+      const uint32_t bt = r / H, h = r - bt * H, b = bt / n, t = bt - b * n;
+      ov[u] = *reinterpret_cast<const uint4*>(a.o + b * a.os_b + t * a.os_t + h * a.os_h + c);
+      dv[u] = *reinterpret_cast<const uint4*>(a.d_o + b * a.ds_b + t * a.ds_t + h * a.ds_h + c);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t x[4] = {ov[u].x, ov[u].y, ov[u].z, ov[u].w};
+      const uint32_t y[4] = {dv[u].x, dv[u].y, dv[u].z, dv[u].w};
+      float s = 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        s += u2f(x[q] << 16) * u2f(y[q] << 16) +
+             u2f(x[q] & 0xFFFF0000u) * u2f(y[q] & 0xFFFF0000u);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if ((lane & 15) == 0 && r0 + 16 * u < rows) delta[r0 + 16 * u] = s;
+    }
     return;
   }
   __shared__ int2 wsum[8], carry;
@@ -667,8 +677,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-// dv, dk of the cut blocks: their chunks' sums added in chunk order.  One block
-// per (batch, group, key block of the cut ones' range).
+// dv, dk of the cut blocks: their chunks' sums added in chunk order, 4 values a
+// thread.  blockIdx.x: (batch, group, key block of the cut ones' range).
 __global__ void __launch_bounds__(256)
     window_bwd_join_kernel(const __grid_constant__ WindowBwdArgs p, int32_t c_lo, int32_t n_c) {
   const WindowArgs& a = p.w;
@@ -677,30 +687,28 @@ __global__ void __launch_bounds__(256)
   wb_query_tiles(a, c, first, count);
   const int32_t k = wb_chunks(count, p.chunk);
   if (k == 1) return;
+  const int i = blockIdx.y * 256 + threadIdx.x;             // of 2 x 128 x 32 float4
   const float4* src = reinterpret_cast<const float4*>(p.part) +
-                      ((int64_t)bg * p.n_part + __ldg(p.pbase + c)) * 8192;
-  for (int i = threadIdx.x; i < 8192; i += 256) {
-    float4 t = __ldg(src + i);
-#pragma unroll 4
-    for (int32_t j = 1; j < k; ++j) {
-      const float4 u = __ldg(src + (int64_t)j * 8192 + i);
-      t.x += u.x;
-      t.y += u.y;
-      t.z += u.z;
-      t.w += u.w;
-    }
-    const int64_t key = (int64_t)c * 128 + ((i >> 5) & 127);
-    if (key >= a.n_kv) continue;
-    __nv_bfloat16* dst = (i >= 4096 ? a.dk : a.dv) +
-                         ((int64_t)bg * a.n_kv + key) * kHeadDim + 4 * (i & 31);
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+                      ((int64_t)bg * p.n_part + __ldg(p.pbase + c)) * 8192 + i;
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int32_t j = 0; j < k; ++j) {
+    const float4 u = __ldg(src + (int64_t)j * 8192);
+    t.x += u.x;
+    t.y += u.y;
+    t.z += u.z;
+    t.w += u.w;
   }
+  const int64_t key = (int64_t)c * 128 + ((i >> 5) & 127);
+  if (key >= a.n_kv) return;
+  __nv_bfloat16* dst =
+      (i >= 4096 ? a.dk : a.dv) + ((int64_t)bg * a.n_kv + key) * kHeadDim + 4 * (i & 31);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
 }
 
 size_t window_attn_bwd_workspace(const WindowArgs& a) {
   const WbPlan p = wb_plan(a);
-  if (p.n_dkv + p.n_dq > 0x7FFFFF00) return 0;
+  if (p.n_dkv + p.n_dq > 0x7FFFFF00 || a.batch * a.n_q * a.G * a.R > 0x7FFFFF00) return 0;
   return pad32((size_t)a.batch * a.n_q * a.G * a.R * 4) + pad32((size_t)p.n_cut * 8) +
          pad32((size_t)p.nblk * 4) + 32 +
          (size_t)a.batch * a.G * p.n_part * 2 * 128 * 128 * sizeof(float);
@@ -743,7 +751,7 @@ cudaError_t launch_window_attn_bwd(const CUtensorMap& tm_q, const CUtensorMap& t
   p.n_dkv = (int32_t)pl.n_dkv;
   p.n_all = (int32_t)(pl.n_dkv + pl.n_dq);
   const int64_t rows = a.batch * a.n_q * a.G * a.R;
-  window_bwd_prep_kernel<<<(unsigned)((rows + 7) / 8 + 1), 256, 0, st>>>(
+  window_bwd_prep_kernel<<<(unsigned)((rows + kWbPrepRows - 1) / kWbPrepRows + 1), 256, 0, st>>>(
       a, delta, table, pbase, p.counter, pl.chunk, p.nblk);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   window_attn_bwd_kernel<<<(unsigned)min64(p.n_all, sms), kWbThreads, kWbSmemBytes, st>>>(
@@ -751,8 +759,8 @@ cudaError_t launch_window_attn_bwd(const CUtensorMap& tm_q, const CUtensorMap& t
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (pl.n_part > 0) {
     const int32_t n_c = (int32_t)(pl.c_hi - pl.c_lo);
-    window_bwd_join_kernel<<<(unsigned)(a.batch * a.G * n_c), 256, 0, st>>>(p, (int32_t)pl.c_lo,
-                                                                            n_c);
+    window_bwd_join_kernel<<<dim3((unsigned)(a.batch * a.G * n_c), 32), 256, 0, st>>>(
+        p, (int32_t)pl.c_lo, n_c);
   }
   return cudaGetLastError();
 }
