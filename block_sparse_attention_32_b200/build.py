@@ -1,8 +1,10 @@
-"""Build ``libmsa.so`` (the C-ABI library of the MSA hot path) in-tree.
+"""Build ``libmsa.so`` (the C-ABI library of the MSA hot path) and ``msa_calls.so``
+(Python calls of the operators around the path) in-tree.
 
 Every CUDA source under ``csrc/`` is compiled for sm_100a only
 (``-gencode arch=compute_100a,code=sm_100a``) and linked into
-``block_sparse_attention_32_b200/lib/libmsa.so``.  Run
+``block_sparse_attention_32_b200/lib/libmsa.so``; ``csrc/calls.cpp`` is compiled
+against torch's headers and linked to it.  Run
 ``python -m block_sparse_attention_32_b200.build`` (or call ``build()``).
 """
 from __future__ import annotations
@@ -18,6 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(OUT_DIR, "libmsa.so")
+CALLS = os.path.join(OUT_DIR, "msa_calls.so")
 OBJ_DIR = os.path.join(ROOT, "_build", "msa")
 
 SOURCES = ["msa_api.cu", "index_score.cu", "topk.cu", "block_lists.cu", "block_lists_noalloc.cu",
@@ -81,7 +84,35 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    build_calls(force)
     return LIB
+
+
+def build_calls(force: bool = False) -> str:
+    """Compile (if needed) and return the path of msa_calls.so."""
+    src = os.path.join(CSRC, "calls.cpp")
+    if not force and not _stale(CALLS, [src, os.path.join(ROOT, "include", "msa.h")]):
+        return CALLS
+    import sysconfig
+
+    import torch
+    troot = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(troot, "include"),
+           "-isystem", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(cuda, "include"), src, "-o", tmp,
+           "-L", OUT_DIR, "-l:libmsa.so", "-L", os.path.join(troot, "lib"), "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 if __name__ == "__main__":

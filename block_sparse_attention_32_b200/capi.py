@@ -9,6 +9,7 @@ first use: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -16,6 +17,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libmsa.so")
+CALLS_PATH = os.path.join(_HERE, "lib", "msa_calls.so")
 
 BLOCK = 128
 TOPK = 16
@@ -351,129 +353,49 @@ def msa_index_score_maxpool_e4m3(d: Dims, q_idx8, k_idx8, scale_q, scale_k, pool
 
 
 # ---------------------------------------------------------------------------
-# operators around the sparse path
+# operators around the sparse path: checks and marshalling in lib/msa_calls.so
+# (csrc/calls.cpp).  Tensors that do not fit together raise ValueError, a refusal
+# of the C entry point MSAError; every tensor has to be on the current device,
+# whose current stream the call is enqueued on.
 # ---------------------------------------------------------------------------
-def _need(cond, what):
-    if not cond:
-        raise ValueError(what)
+_calls = None
 
 
-def _on_current(*tensors):
-    """The call is enqueued on the current device's current stream: every
-    tensor has to live there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None:
-            _need(t.is_cuda and t.get_device() == dev,
-                  f"every tensor must be on the current device cuda:{dev}")
-
-
-def _rows(name, t, shape, dtype=torch.bfloat16):
-    """A [B, T, H, D] tensor as msa_tensor, after checking its shape and type."""
-    _need(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    _need(t.dtype == dtype, f"{name}: {t.dtype}, expected {dtype}")
-    _need(t.stride(3) == 1, f"{name}: the last dimension must be contiguous")
-    return Tensor(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
-
-
-def _heads_first(name, t, shape, dtype=torch.bfloat16):
-    """A [B, H, T, D] tensor as msa_tensor."""
-    _need(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    return _rows(name, t.transpose(1, 2), (shape[0], shape[2], shape[1], shape[3]), dtype)
-
-
-def _flat(name, t, shape, dtype):
-    """A contiguous tensor of the given shape (None: passed as a null pointer)."""
-    if t is None:
-        return 0
-    _need(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    _need(t.dtype == dtype and t.is_contiguous(), f"{name}: must be contiguous {dtype}")
-    return t.data_ptr()
-
-
-_NO_TENSOR = Tensor(0, 0, 0, 0)
-
-
-def _norm_rope_dims(q, k, table, positions, pos0, eps, interleaved):
-    some = q if q is not None else k
-    _need(some is not None and some.dim() == 4, "q or k must be given, [B, T, H, D]")
-    B, T, D = some.shape[0], some.shape[1], some.shape[3]
-    rot = 0 if table is None else table.shape[1]
-    return NormRopeDims(B, T, pos0, 0 if q is None else q.shape[2],
-                        0 if k is None else k.shape[2], D, rot, 1 if interleaved else 0, eps)
-
-
-def _norm_rope_common(d, q, k, w_q, w_k, table, positions):
-    B, T, D = d.batch, d.n_tok, d.d
-    n_pos = 0 if table is None else table.shape[0]
-    if table is None and positions is None:
-        n_pos = d.pos0 + T                 # no rotation: every position is in range
-    elif table is None:
-        n_pos = (1 << 63) - 1
-    return (_NO_TENSOR if q is None else _rows("q", q, (B, T, d.h_q, D)),
-            _NO_TENSOR if k is None else _rows("k", k, (B, T, d.h_k, D)),
-            _flat("w_q", w_q, (D,), torch.float32), _flat("w_k", w_k, (D,), torch.float32),
-            _flat("table", table, (n_pos, d.rot), torch.float32), n_pos,
-            _flat("positions", positions, (B, T), torch.int64))
-
-
-def _out_rows(name, t, like, shape):
-    if like is None:
-        return _NO_TENSOR
-    _need(t is not None, f"{name} is missing")
-    return _rows(name, t, shape)
+def calls():
+    """The msa_calls module (raises if it has not been built)."""
+    global _calls
+    if _calls is None:
+        with _lock:
+            if not os.path.exists(CALLS_PATH):
+                raise RuntimeError(
+                    f"{CALLS_PATH} is missing: build it with "
+                    "`python -m block_sparse_attention_32_b200.build` (no fallback exists)")
+            spec = importlib.util.spec_from_file_location("msa_calls", CALLS_PATH)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            _calls = mod
+    return _calls
 
 
 def msa_qk_norm_rope(q, k, w_q, w_k, table, q_out, k_out, positions=None, pos0=0, eps=1e-6,
                      interleaved=False, dev_err=None):
     """q [B,T,Hq,D], k [B,T,Hk,D] (either may be None) -> q_out [B,T,Hq,D], k_out
     [B,Hk,T,D] (the attention's layout; any strides).  table fp32 [n_pos, rot]."""
-    d = _norm_rope_dims(q, k, table, positions, pos0, eps, interleaved)
-    _on_current(q, k, w_q, w_k, table, q_out, k_out, positions, dev_err)
-    qt, kt, wq, wk, tab, n_pos, pos = _norm_rope_common(d, q, k, w_q, w_k, table, positions)
-    qo = _out_rows("q_out", q_out, q, (d.batch, d.n_tok, d.h_q, d.d))
-    _need(k is None or k_out is not None, "k_out is missing")
-    ko = _NO_TENSOR if k is None else _heads_first("k_out", k_out,
-                                                   (d.batch, d.h_k, d.n_tok, d.d))
-    _check("msa_qk_norm_rope",
-           lib().msa_qk_norm_rope(ctypes.byref(d), qt, kt, wq, wk, tab, n_pos, pos, qo, ko,
-                                  _ptr(dev_err), _stream()))
+    st = calls().norm_rope(q, k, w_q, w_k, table, q_out, k_out, positions, pos0, eps, interleaved,
+                           dev_err)
+    if st:
+        raise MSAError("msa_qk_norm_rope", st)
 
 
-def paged_kv(k_pages, v_pages, block_table, seq_lens=None) -> PagedKV:
-    """Descriptor of a paged cache: k_pages, v_pages bf16 [n_pages, h_kv,
-    page_size, 128] of equal strides (a permuted view when tokens are stored
-    outermost), block_table int32 [B, pages per sequence], seq_lens int32 [B]."""
-    _on_current(k_pages, v_pages, block_table, seq_lens)
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _need(t.dim() == 4 and t.shape[3] == HEAD_DIM and t.dtype == torch.bfloat16,
-              f"{name}: must be bf16 [n_pages, h_kv, page_size, {HEAD_DIM}]")
-        _need(t.stride(3) == 1, f"{name}: the last dimension must be contiguous")
-    _need(k_pages.shape == v_pages.shape and k_pages.stride() == v_pages.stride(),
-          "k_pages and v_pages must have the same shape and strides")
-    _need(block_table.dim() == 2, "block_table: must be [B, pages per sequence]")
-    B, per = block_table.shape
-    _flat("block_table", block_table, (B, per), torch.int32)
-    _flat("seq_lens", seq_lens, (B,), torch.int32)
-    return PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.shape[0], k_pages.stride(0),
-                   k_pages.stride(2), k_pages.stride(1), block_table.data_ptr(), per,
-                   _ptr(seq_lens), k_pages.shape[2], k_pages.shape[1])
-
-
-def msa_qk_norm_rope_paged(q, k, v, w_q, w_k, table, q_out, cache: PagedKV, cache_batch,
+def msa_qk_norm_rope_paged(q, k, v, w_q, w_k, table, q_out, k_pages, v_pages, block_table,
                            positions=None, pos0=0, eps=1e-6, interleaved=False, dev_err=None):
-    """As msa_qk_norm_rope, keys and the values v [B,T,Hk,128] into the paged cache
-    (cache_batch: the sequences its block table has)."""
-    _need(k is not None and v is not None, "k and v must be given")
-    d = _norm_rope_dims(q, k, table, positions, pos0, eps, interleaved)
-    _on_current(q, k, v, w_q, w_k, table, q_out, positions, dev_err)
-    _need(cache_batch == d.batch, "the block table must have a row for each sequence")
-    qt, kt, wq, wk, tab, n_pos, pos = _norm_rope_common(d, q, k, w_q, w_k, table, positions)
-    vt = _rows("v", v, (d.batch, d.n_tok, d.h_k, d.d))
-    qo = _out_rows("q_out", q_out, q, (d.batch, d.n_tok, d.h_q, d.d))
-    _check("msa_qk_norm_rope_paged",
-           lib().msa_qk_norm_rope_paged(ctypes.byref(d), qt, kt, vt, wq, wk, tab, n_pos, pos, qo,
-                                        ctypes.byref(cache), _ptr(dev_err), _stream()))
+    """As msa_qk_norm_rope, keys and the values v [B,T,Hk,128] into the pages
+    [n_pages, h_kv, page_size, 128] (K and V of equal strides; a permuted view when
+    tokens are stored outermost) that block_table int32 [B, pages per sequence] names."""
+    st = calls().norm_rope_paged(q, k, v, w_q, w_k, table, q_out, k_pages, v_pages, block_table,
+                                 positions, pos0, eps, interleaved, dev_err)
+    if st:
+        raise MSAError("msa_qk_norm_rope_paged", st)
 
 
 def msa_qk_norm_rope_bwd_workspace(d_head) -> int:
@@ -485,58 +407,32 @@ def msa_qk_norm_rope_bwd(q, k, w_q, w_k, table, d_q, d_k, dx_q, dx_k, dw_q, dw_k
                          positions=None, pos0=0, eps=1e-6, interleaved=False, dev_err=None):
     """d_q [B,T,Hq,D], d_k [B,Hk,T,D] (both bf16 or both fp32) -> dx_q [B,T,Hq,D], dx_k
     [B,T,Hk,D] bf16, dw_q, dw_k [D] fp32 (None: not wanted)."""
-    d = _norm_rope_dims(q, k, table, positions, pos0, eps, interleaved)
-    _on_current(q, k, w_q, w_k, table, d_q, d_k, dx_q, dx_k, dw_q, dw_k, ws, positions, dev_err)
-    qt, kt, wq, wk, tab, n_pos, pos = _norm_rope_common(d, q, k, w_q, w_k, table, positions)
-    _need((q is None or d_q is not None) and (k is None or d_k is not None),
-          "an upstream gradient is missing")
-    t = (d_q if q is not None else d_k).dtype
-    _need(t in (torch.bfloat16, torch.float32), "gradients must be bf16 or fp32")
-    dq = _NO_TENSOR if q is None else _rows("d_q", d_q, (d.batch, d.n_tok, d.h_q, d.d), t)
-    dk = _NO_TENSOR if k is None else _heads_first("d_k", d_k,
-                                                   (d.batch, d.h_k, d.n_tok, d.d), t)
-    xq = _out_rows("dx_q", dx_q, q, (d.batch, d.n_tok, d.h_q, d.d))
-    xk = _out_rows("dx_k", dx_k, k, (d.batch, d.n_tok, d.h_k, d.d))
-    nbytes = ws.numel() * ws.element_size()
-    _check("msa_qk_norm_rope_bwd",
-           lib().msa_qk_norm_rope_bwd(ctypes.byref(d), qt, kt, wq, wk, tab, n_pos, pos, dq, dk,
-                                      1 if t == torch.float32 else 0, xq, xk,
-                                      _flat("dw_q", dw_q, (d.d,), torch.float32),
-                                      _flat("dw_k", dw_k, (d.d,), torch.float32), _ptr(ws),
-                                      nbytes, _ptr(dev_err), _stream()))
+    st = calls().norm_rope_bwd(q, k, w_q, w_k, table, d_q, d_k, dx_q, dx_k, dw_q, dw_k, ws,
+                               positions, pos0, eps, interleaved, dev_err)
+    if st:
+        raise MSAError("msa_qk_norm_rope_bwd", st)
 
 
 def msa_paged_decode_attn_workspace(d: Dims) -> int:
     return int(lib().msa_paged_decode_attn_workspace(ctypes.byref(d)))
 
 
-def msa_paged_decode_attn(d: Dims, q, cache: PagedKV, cache_batch, out, lse, ws, window=0,
-                          n_sink=0, dev_err=None):
+def msa_paged_decode_attn(d: Dims, q, k_pages, v_pages, block_table, seq_lens, out, lse, ws,
+                          window=0, n_sink=0, dev_err=None):
     """One new token per sequence over the paged cache: q, out [B,1,H,128] bf16,
-    lse [B,1,H] fp32."""
-    _on_current(q, out, lse, ws, dev_err)
-    _need(cache_batch == d.batch, "the block table must have a row for each sequence")
-    shape = (d.batch, 1, d.h_q, HEAD_DIM)
-    qt = _rows("q", q, shape)
-    _check("msa_paged_decode_attn",
-           lib().msa_paged_decode_attn(ctypes.byref(d), window, n_sink, qt, ctypes.byref(cache),
-                                       _flat("out", out, shape, torch.bfloat16),
-                                       _flat("lse", lse, shape[:3], torch.float32), _ptr(ws),
-                                       ws.numel() * ws.element_size(), _ptr(dev_err), _stream()))
+    lse [B,1,H] fp32, seq_lens int32 [B]."""
+    st = calls().paged_decode(d, window, n_sink, q, k_pages, v_pages, block_table, seq_lens, out,
+                              lse, ws, dev_err)
+    if st:
+        raise MSAError("msa_paged_decode_attn", st)
 
 
 def msa_window_attn_fwd(d: Dims, window, n_sink, q, k, v, out, lse, kv_len=None, dev_err=None):
     """Sliding-window attention with sinks: q, out [B,n_q,H,128], k, v [B,G,n_kv,128]
     bf16, lse [B,n_q,H] fp32, kv_len int32 [B] (padded batch) or None."""
-    _on_current(q, k, v, out, lse, kv_len, dev_err)
-    qs, ks = (d.batch, d.n_q, d.h_q, HEAD_DIM), (d.batch, d.h_kv, d.n_kv, HEAD_DIM)
-    _check("msa_window_attn_fwd",
-           lib().msa_window_attn_fwd(ctypes.byref(d), window, n_sink, _rows("q", q, qs),
-                                     _heads_first("k", k, ks), _heads_first("v", v, ks),
-                                     _flat("kv_len", kv_len, (d.batch,), torch.int32),
-                                     _flat("out", out, qs, torch.bfloat16),
-                                     _flat("lse", lse, qs[:3], torch.float32), _ptr(dev_err),
-                                     _stream()))
+    st = calls().window_fwd(d, window, n_sink, q, k, v, out, lse, kv_len, dev_err)
+    if st:
+        raise MSAError("msa_window_attn_fwd", st)
 
 
 def msa_window_attn_bwd_workspace(d: Dims, window, n_sink) -> int:
@@ -546,15 +442,7 @@ def msa_window_attn_bwd_workspace(d: Dims, window, n_sink) -> int:
 def msa_window_attn_bwd(d: Dims, window, n_sink, q, k, v, o, d_o, lse, dq, dk, dv, ws,
                         kv_len=None, dev_err=None):
     """dq [B,n_q,H,128], dk, dv [B,G,n_kv,128] (bf16) for the upstream d_o (bf16)."""
-    _on_current(q, k, v, o, d_o, lse, dq, dk, dv, ws, kv_len, dev_err)
-    qs, ks = (d.batch, d.n_q, d.h_q, HEAD_DIM), (d.batch, d.h_kv, d.n_kv, HEAD_DIM)
-    _check("msa_window_attn_bwd",
-           lib().msa_window_attn_bwd(ctypes.byref(d), window, n_sink, _rows("q", q, qs),
-                                     _heads_first("k", k, ks), _heads_first("v", v, ks),
-                                     _rows("o", o, qs), _rows("d_o", d_o, qs),
-                                     _flat("lse", lse, qs[:3], torch.float32),
-                                     _flat("kv_len", kv_len, (d.batch,), torch.int32),
-                                     _flat("dq", dq, qs, torch.bfloat16),
-                                     _flat("dk", dk, ks, torch.bfloat16),
-                                     _flat("dv", dv, ks, torch.bfloat16), _ptr(ws),
-                                     ws.numel() * ws.element_size(), _ptr(dev_err), _stream()))
+    st = calls().window_bwd(d, window, n_sink, q, k, v, o, d_o, lse, dq, dk, dv, ws, kv_len,
+                            dev_err)
+    if st:
+        raise MSAError("msa_window_attn_bwd", st)

@@ -2,9 +2,39 @@
 // the sparse path (norm + rotation, paged decode, window attention).
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace msa {
+
+// Host: the current device's SM count, after setting the kernel's shared-memory
+// limit (and, with regs > 0, checking its compiled register count, which a kernel
+// that shares registers out among its warpgroups relies on).  Done once per
+// device; `done` is the kernel's own table.
+struct KernelSetup {
+  std::atomic<int> sms[64];
+};
+inline cudaError_t kernel_setup(KernelSetup& done, const void* kernel, int smem, int regs,
+                                int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool kept = dev >= 0 && dev < 64;
+  if (kept && (*sms = done.sms[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+  if ((e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return e;
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
+      cudaSuccess)
+    return e;
+  if (regs > 0) {
+    cudaFuncAttributes attr;
+    if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
+    if (attr.numRegs != regs) return cudaErrorInvalidConfiguration;
+  }
+  if (kept) done.sms[dev].store(*sms, std::memory_order_release);
+  return cudaSuccess;
+}
 
 struct NormRopeArgs {
   const __nv_bfloat16* src[3];   // q, k, v (v: paged form only, copied)

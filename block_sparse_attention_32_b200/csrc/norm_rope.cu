@@ -24,17 +24,64 @@
 
 namespace msa {
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+// A lane's 8 features as four packed fp32 pairs, arranged so that the partners of
+// pair (0, 1 | 2, 3) sit in v[0] and v[2] (v[1] and v[3]), whatever the pairing.
+struct Row8 {
+  uint64_t v[4];
+};
+__device__ __forceinline__ uint64_t dup_f32x2(float x) {
+  return pack_f32x2(__float_as_uint(x), __float_as_uint(x));
+}
+__device__ __forceinline__ float sum_f32x2(uint64_t x) {
+  float a, b;
+  unpack_f32x2(x, a, b);
+  return a + b;
+}
+__device__ __forceinline__ uint64_t neg_f32x2(uint64_t x) { return x ^ 0x8000000080000000ull; }
+
+template <bool kInter>
+__device__ __forceinline__ void unpack8(const uint4& u, Row8& x) {
+  constexpr uint32_t kHi = 0xFFFF0000u;
+  if (kInter) {                       // a word holds both partners of a pair
+    x.v[0] = pack_f32x2(u.x << 16, u.y << 16);
+    x.v[2] = pack_f32x2(u.x & kHi, u.y & kHi);
+    x.v[1] = pack_f32x2(u.z << 16, u.w << 16);
+    x.v[3] = pack_f32x2(u.z & kHi, u.w & kHi);
+  } else {
+    x.v[0] = pack_f32x2(u.x << 16, u.x & kHi);
+    x.v[1] = pack_f32x2(u.y << 16, u.y & kHi);
+    x.v[2] = pack_f32x2(u.z << 16, u.z & kHi);
+    x.v[3] = pack_f32x2(u.w << 16, u.w & kHi);
   }
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
+template <bool kInter>
+__device__ __forceinline__ uint4 pack8(const Row8& x) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack_f32x2(x.v[i], f[2 * i], f[2 * i + 1]);
+  if (kInter)
+    return make_uint4(pack_bf16x2(f[0], f[4]), pack_bf16x2(f[1], f[5]), pack_bf16x2(f[2], f[6]),
+                      pack_bf16x2(f[3], f[7]));
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+// two runs of four fp32 values (o0.., o1..)
+template <bool kInter>
+__device__ __forceinline__ void arrange8(const float4& a, const float4& b, Row8& x) {
+  auto pk = [](float lo, float hi) {
+    return pack_f32x2(__float_as_uint(lo), __float_as_uint(hi));
+  };
+  if (kInter) {
+    x.v[0] = pk(a.x, a.z);
+    x.v[2] = pk(a.y, a.w);
+    x.v[1] = pk(b.x, b.z);
+    x.v[3] = pk(b.y, b.w);
+  } else {
+    x.v[0] = pk(a.x, a.y);
+    x.v[1] = pk(a.z, a.w);
+    x.v[2] = pk(b.x, b.y);
+    x.v[3] = pk(b.z, b.w);
+  }
 }
 
 // offsets of a lane's two runs of 4 features; `turns`: they are rotated
@@ -78,38 +125,48 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, const LanePos& l, co
 }
 
 // cosines and sines of the lane's 4 pairs (1, 0 where nothing turns)
+struct Angles {
+  uint64_t c[2], s[2];
+};
 __device__ __forceinline__ void load_angles(const float* __restrict__ row, int rot,
-                                            const LanePos& l, bool want, float (&c)[4],
-                                            float (&s)[4]) {
-  float4 cv = make_float4(1.f, 1.f, 1.f, 1.f), sv = make_float4(0.f, 0.f, 0.f, 0.f);
+                                            const LanePos& l, bool want, Angles& a) {
+  a.c[0] = a.c[1] = dup_f32x2(1.f);
+  a.s[0] = a.s[1] = 0ull;
   if (want && l.turns) {
-    cv = __ldg(reinterpret_cast<const float4*>(row + l.ang));
-    sv = __ldg(reinterpret_cast<const float4*>(row + (rot >> 1) + l.ang));
+    const ulonglong2 c = __ldg(reinterpret_cast<const ulonglong2*>(row + l.ang));
+    const ulonglong2 s = __ldg(reinterpret_cast<const ulonglong2*>(row + (rot >> 1) + l.ang));
+    a.c[0] = c.x;
+    a.c[1] = c.y;
+    a.s[0] = s.x;
+    a.s[1] = s.y;
   }
-  c[0] = cv.x; c[1] = cv.y; c[2] = cv.z; c[3] = cv.w;
-  s[0] = sv.x; s[1] = sv.y; s[2] = sv.z; s[3] = sv.w;
 }
+template <bool kInter>
 __device__ __forceinline__ void load_weights(const float* __restrict__ w, const LanePos& l,
-                                             float (&v)[8]) {
+                                             Row8& v) {
   float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = a;
   if (w != nullptr) {
     a = __ldg(reinterpret_cast<const float4*>(w + l.o0));
     b = __ldg(reinterpret_cast<const float4*>(w + l.o1));
   }
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  arrange8<kInter>(a, b, v);
 }
 
 // turns y by the angles (kSign 1) or back (-1)
-template <bool kInter, int kSign>
-__device__ __forceinline__ void rotate8(float (&y)[8], const float (&c)[4], const float (&s)[4]) {
+template <int kSign>
+__device__ __forceinline__ void rotate8(Row8& y, const Angles& a) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int ia = kInter ? 2 * i : i, ib = kInter ? 2 * i + 1 : i + 4;
-    const float a = y[ia], b = y[ib], sn = kSign > 0 ? s[i] : -s[i];
-    y[ia] = a * c[i] - b * sn;
-    y[ib] = b * c[i] + a * sn;
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t p = y.v[i], q = y.v[i + 2];
+    const uint64_t sp = kSign > 0 ? a.s[i] : neg_f32x2(a.s[i]), sm = neg_f32x2(sp);
+    y.v[i] = fma_f32x2(q, sm, mul_f32x2(p, a.c[i]));
+    y.v[i + 2] = fma_f32x2(p, sp, mul_f32x2(q, a.c[i]));
   }
+}
+__device__ __forceinline__ float dot8(const Row8& a, const Row8& b) {
+  const uint64_t s0 = fma_f32x2(a.v[1], b.v[1], mul_f32x2(a.v[0], b.v[0]));
+  const uint64_t s1 = fma_f32x2(a.v[3], b.v[3], mul_f32x2(a.v[2], b.v[2]));
+  return sum_f32x2(add_f32x2(s0, s1));
 }
 
 template <int kLanes>
@@ -182,24 +239,23 @@ __global__ void __launch_bounds__(kNrThreads)
       dst += b * a.ds_b[kind] + i * a.ds_t[kind];
     }
   }
-  float c[4], s[4], w[8];
+  Angles ang;
+  Row8 w;
   const bool norm = !kPaged || kind < 2;
-  load_angles(a.table + (live ? pos : 0) * a.rot, a.rot, lp, live && norm, c, s);
-  load_weights(norm ? a.w[kPaged ? min(kind, 1) : kind] : nullptr, lp, w);
+  load_angles(a.table + (live ? pos : 0) * a.rot, a.rot, lp, live && norm, ang);
+  load_weights<kInter>(norm ? a.w[kPaged ? min(kind, 1) : kind] : nullptr, lp, w);
 #pragma unroll
   for (int u = 0; u < kNrHeads; ++u) {
     if (u >= a.hc) break;                           // the same for every lane
-    float x[8];
-    unpack8(v[u], x);
-    float ss = 0.f;
+    Row8 x;
+    unpack8<kInter>(v[u], x);
+    const float ss = row_sum<kLanes>(dot8(x, x));
+    const uint64_t r = dup_f32x2(rsqrtf(ss * (1.f / kD) + a.eps));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
-    ss = row_sum<kLanes>(ss);
-    const float r = rsqrtf(ss * (1.f / kD) + a.eps);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
-    rotate8<kInter, 1>(x, c, s);
-    if (live && h0 + u < h1) store_row<kInter>(dst + u * a.ds_h[kind], lp, norm ? pack8(x) : v[u]);
+    for (int j = 0; j < 4; ++j) x.v[j] = mul_f32x2(mul_f32x2(x.v[j], r), w.v[j]);
+    rotate8<1>(x, ang);
+    if (live && h0 + u < h1)
+      store_row<kInter>(dst + u * a.ds_h[kind], lp, norm ? pack8<kInter>(x) : v[u]);
   }
 }
 
@@ -217,17 +273,13 @@ __device__ __forceinline__ void load_dy(const void* p, int64_t off, const LanePo
     v[0] = load_row<kInter>(reinterpret_cast<const __nv_bfloat16*>(p) + off, l);
   }
 }
-template <bool kF32>
-__device__ __forceinline__ void unpack_dy(const uint4 (&v)[2], float (&y)[8]) {
-  if (kF32) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      y[4 * j] = u2f(v[j].x); y[4 * j + 1] = u2f(v[j].y);
-      y[4 * j + 2] = u2f(v[j].z); y[4 * j + 3] = u2f(v[j].w);
-    }
-  } else {
-    unpack8(v[0], y);
-  }
+template <bool kInter, bool kF32>
+__device__ __forceinline__ void unpack_dy(const uint4 (&v)[2], Row8& y) {
+  if (kF32)
+    arrange8<kInter>(make_float4(u2f(v[0].x), u2f(v[0].y), u2f(v[0].z), u2f(v[0].w)),
+                     make_float4(u2f(v[1].x), u2f(v[1].y), u2f(v[1].z), u2f(v[1].w)), y);
+  else
+    unpack8<kInter>(v[0], y);
 }
 
 // Persistent blocks over the items, all of the queries' before the keys': the
@@ -245,11 +297,11 @@ __global__ void __launch_bounds__(kNrThreads, 2)
   __shared__ float red[kGroups][kD + 4];
   const int ln = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
   const LanePos lp = lane_pos<kInter>(ln, a.rot);
-  float dwq[8], g[8], w[8];
+  Row8 dwq, g, w;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) dwq[j] = g[j] = 0.f;
+  for (int j = 0; j < 4; ++j) dwq.v[j] = g.v[j] = 0ull;
   int cur = 0;                                      // kind that g belongs to
-  load_weights(a.w[0], lp, w);
+  load_weights<kInter>(a.w[0], lp, w);
   const uint32_t n_items = (uint32_t)a.n_items;
   const uint32_t nq = (uint32_t)(a.batch * a.n_tok) * a.chunks[0];
   const uint32_t step = gridDim.x * kGroups;
@@ -267,11 +319,11 @@ __global__ void __launch_bounds__(kNrThreads, 2)
     if (in && kind != cur) {
       cur = kind;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        dwq[j] = g[j];
-        g[j] = 0.f;
+      for (int j = 0; j < 4; ++j) {
+        dwq.v[j] = g.v[j];
+        g.v[j] = 0ull;
       }
-      load_weights(a.w[1], lp, w);
+      load_weights<kInter>(a.w[1], lp, w);
     }
     const int64_t pos = in ? token_pos(a, bt, i) : -1;
     const bool live = pos >= 0;
@@ -279,8 +331,8 @@ __global__ void __launch_bounds__(kNrThreads, 2)
     const __nv_bfloat16* src = a.src[kind] + b * a.ss_b[kind] + i * a.ss_t[kind];
     __nv_bfloat16* dst = a.dst[kind] + b * a.ds_b[kind] + i * a.ds_t[kind];
     const int64_t yo = b * p.ys_b[kind] + i * p.ys_t[kind];
-    float c[4], s[4];
-    load_angles(a.table + (live ? pos : 0) * a.rot, a.rot, lp, live, c, s);
+    Angles ang;
+    load_angles(a.table + (live ? pos : 0) * a.rot, a.rot, lp, live, ang);
     for (int hb = 0; hb < a.hc; hb += kU) {
       uint4 xv[kU], yv[kU][2];
 #pragma unroll
@@ -296,37 +348,42 @@ __global__ void __launch_bounds__(kNrThreads, 2)
       for (int u = 0; u < kU; ++u) {
         const int h = h0 + hb + u;
         if (hb + u >= a.hc) break;                  // the same for every lane
-        float x[8], y[8];
-        unpack8(xv[u], x);
-        unpack_dy<kF32>(yv[u], y);
-        rotate8<kInter, -1>(y, c, s);
-        float ss = 0.f, sy = 0.f;
+        Row8 x, y, yw;
+        unpack8<kInter>(xv[u], x);
+        unpack_dy<kInter, kF32>(yv[u], y);
+        rotate8<-1>(y, ang);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          ss += x[j] * x[j];
-          sy += x[j] * y[j] * w[j];
-        }
-        ss = row_sum<kLanes>(ss);
-        sy = row_sum<kLanes>(sy);
+        for (int j = 0; j < 4; ++j) yw.v[j] = mul_f32x2(y.v[j], w.v[j]);
+        const float ss = row_sum<kLanes>(dot8(x, x)), sy = row_sum<kLanes>(dot8(x, yw));
         // absent rows (zeros) add nothing, with eps = 0 too (there r is infinite)
         const float r = live && h < h1 ? rsqrtf(ss * (1.f / kD) + a.eps) : 0.f;
-        const float m = sy * r * (1.f / kD);         // mean(dz w xh)
+        // dx = r (dz w) - x r^3 mean(dz w x)
+        const float m = sy * r * (1.f / kD);
+        const uint64_t r2 = dup_f32x2(r), f2 = dup_f32x2(-r * r * m);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float xh = x[j] * r;
-          g[j] += y[j] * xh;
-          x[j] = r * (y[j] * w[j] - xh * m);
+        for (int j = 0; j < 4; ++j) {
+          g.v[j] = fma_f32x2(y.v[j], mul_f32x2(x.v[j], r2), g.v[j]);
+          x.v[j] = fma_f32x2(x.v[j], f2, mul_f32x2(yw.v[j], r2));
         }
-        if (live && h < h1) store_row<kInter>(dst + h * a.ds_h[kind], lp, pack8(x));
+        if (live && h < h1)
+          store_row<kInter>(dst + h * a.ds_h[kind], lp, pack8<kInter>(x));
       }
     }
   }
   for (int k = 0; k < 2; ++k) {
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float t = k == 0 ? (cur == 0 ? g[j] : dwq[j]) : (cur == 0 ? 0.f : g[j]);
-      red[grp][(j < 4 ? lp.o0 : lp.o1 - 4) + j] = t;
+    for (int j = 0; j < 4; ++j) {
+      float t[2];
+      unpack_f32x2(k == 0 ? (cur == 0 ? g.v[j] : dwq.v[j]) : (cur == 0 ? 0ull : g.v[j]), t[0],
+                   t[1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // feature of element 2 j + e: the arrangement of Row8 undone
+        const int i = 2 * (j & 1) + e;              // pair of the lane
+        const int f = kInter ? lp.o0 + 2 * i + (j >> 1) : (j < 2 ? lp.o0 : lp.o1) + i;
+        red[grp][f] = t[e];
+      }
     }
     __syncthreads();
     if (threadIdx.x < kD) {

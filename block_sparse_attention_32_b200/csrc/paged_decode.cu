@@ -485,14 +485,10 @@ int32_t paged_decode_tile() { return kPdTile; }
 
 cudaError_t launch_paged_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                 PagedDecodeArgs a, void* ws, cudaStream_t st) {
-  int dev = 0, sms = 0;
-  cudaError_t e;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-    return e;
-  if ((e = cudaFuncSetAttribute(paged_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kPdSmemBytes)) != cudaSuccess)
-    return e;
+  static KernelSetup setup;
+  int sms = 0;
+  cudaError_t e = kernel_setup(setup, reinterpret_cast<const void*>(paged_decode_kernel), kPdSmemBytes, 0, &sms);
+  if (e != cudaSuccess) return e;
   const int grid = sms < kPdMaxBlocks ? sms : kPdMaxBlocks;
   const int64_t workers = (int64_t)grid * kPdWarps;
   uint8_t* p = static_cast<uint8_t*>(ws);

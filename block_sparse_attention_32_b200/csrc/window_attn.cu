@@ -398,18 +398,10 @@ __global__ void __launch_bounds__(kWaThreads, 1)
 cudaError_t launch_window_attn_fwd(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                    const CUtensorMap& tm_v, const WindowArgs& a,
                                    cudaStream_t st) {
-  int dev = 0, sms = 0;
-  cudaError_t e;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-    return e;
-  if ((e = cudaFuncSetAttribute(window_attn_fwd_kernel,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kWaSmemBytes)) !=
-      cudaSuccess)
-    return e;
-  cudaFuncAttributes attr;
-  if ((e = cudaFuncGetAttributes(&attr, window_attn_fwd_kernel)) != cudaSuccess) return e;
-  if (attr.numRegs != kWaRegsAtLaunch) return cudaErrorInvalidConfiguration;
+  static KernelSetup setup;
+  int sms = 0;
+  cudaError_t e = kernel_setup(setup, reinterpret_cast<const void*>(window_attn_fwd_kernel), kWaSmemBytes, kWaRegsAtLaunch, &sms);
+  if (e != cudaSuccess) return e;
   // two row tiles per item overlap their products and softmax; one per item
   // when that would leave SMs without work
   const int64_t tiles = (a.n_q * a.R + 127) / 128;

@@ -717,18 +717,10 @@ size_t window_attn_bwd_workspace(const WindowArgs& a) {
 cudaError_t launch_window_attn_bwd(const CUtensorMap& tm_q, const CUtensorMap& tm_do,
                                    const CUtensorMap& tm_k, const CUtensorMap& tm_v, WindowArgs a,
                                    void* ws, cudaStream_t st) {
-  int dev = 0, sms = 0;
-  cudaError_t e;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-    return e;
-  if ((e = cudaFuncSetAttribute(window_attn_bwd_kernel,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kWbSmemBytes)) !=
-      cudaSuccess)
-    return e;
-  cudaFuncAttributes attr;
-  if ((e = cudaFuncGetAttributes(&attr, window_attn_bwd_kernel)) != cudaSuccess) return e;
-  if (attr.numRegs != kWbRegsAtLaunch) return cudaErrorInvalidConfiguration;
+  static KernelSetup setup;
+  int sms = 0;
+  cudaError_t e = kernel_setup(setup, reinterpret_cast<const void*>(window_attn_bwd_kernel), kWbSmemBytes, kWbRegsAtLaunch, &sms);
+  if (e != cudaSuccess) return e;
   const WbPlan pl = wb_plan(a);
   WindowBwdArgs p;
   p.w = a;

@@ -390,9 +390,6 @@ class PagedCache:
         """Tokens a sequence's table row can hold."""
         return self.block_table.shape[1] * self.k_pages.shape[2]
 
-    def desc(self) -> capi.PagedKV:
-        return capi.paged_kv(self.k_pages, self.v_pages, self.block_table, self.seq_lens)
-
 
 def norm_rope_append(plan: NormRope, q, k, v, positions, q_out, cache: PagedCache, pos0=0,
                      dev_err=None):
@@ -401,9 +398,9 @@ def norm_rope_append(plan: NormRope, q, k, v, positions, q_out, cache: PagedCach
     already map them; seq_lens is the caller's to advance.  Returns q_out."""
     if q is not None and q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    capi.msa_qk_norm_rope_paged(q, k, v, plan.w_q, plan.w_k, plan.table, q_out, cache.desc(),
-                                cache.batch, positions, pos0, plan.eps, plan.interleaved,
-                                dev_err)
+    capi.msa_qk_norm_rope_paged(q, k, v, plan.w_q, plan.w_k, plan.table, q_out, cache.k_pages,
+                                cache.v_pages, cache.block_table, positions, pos0, plan.eps,
+                                plan.interleaved, dev_err)
     return q_out
 
 
@@ -433,8 +430,9 @@ def paged_decode(buf: DecodeBuffers, q, cache: PagedCache, window=0, n_sink=0):
     """Attention of each sequence's newest token (token seq_lens[b] - 1, already in
     the cache) over its pages: all of them, or a window and sinks.  q [B,1,H,128].
     Returns (out bf16 [B,1,H,128], lse fp32 [B,1,H]); an empty sequence gives 0, -inf."""
-    capi.msa_paged_decode_attn(buf.dims, q, cache.desc(), cache.batch, buf.out, buf.lse, buf.ws,
-                               window, n_sink, buf.dev_err)
+    capi.msa_paged_decode_attn(buf.dims, q, cache.k_pages, cache.v_pages, cache.block_table,
+                               cache.seq_lens, buf.out, buf.lse, buf.ws, window, n_sink,
+                               buf.dev_err)
     return buf.out, buf.lse
 
 
