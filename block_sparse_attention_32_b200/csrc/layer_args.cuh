@@ -36,6 +36,30 @@ inline cudaError_t kernel_setup(KernelSetup& done, const void* kernel, int smem,
   return cudaSuccess;
 }
 
+// Dependent launches: the kernel's blocks may take their places while the one
+// before it on the stream still runs (after its grid_launch_dependents), and
+// wait there, in grid_wait, until it is complete and its writes are visible.
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
+                             cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 struct NormRopeArgs {
   const __nv_bfloat16* src[3];   // q, k, v (v: paged form only, copied)
   int64_t ss_b[3], ss_t[3], ss_h[3];
@@ -67,9 +91,10 @@ struct PagedDecodeArgs {
   int64_t qs_b, qs_h;
   const int32_t* block_table;     // [B, table_stride]
   const int32_t* seq_lens;        // [B]
-  int64_t table_stride, n_pages, cap;   // cap: tokens a sequence may have
-  int32_t page_size, batch, G, R;
-  int64_t window, sink;           // window 0: the whole cache
+  int64_t table_stride, n_pages;
+  int32_t cap;                    // tokens a sequence may have (< 2^30)
+  int32_t page_size, page_shift, batch, G, R;   // page_size = 1 << page_shift
+  int32_t window, sink;           // in [1, cap], [0, cap]
   float scale;
   __nv_bfloat16* out;             // [B, 1, H, 128]
   float* lse;                     // [B, 1, H]

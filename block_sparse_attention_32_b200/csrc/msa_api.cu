@@ -909,13 +909,14 @@ msa_status msa_paged_decode_attn(const msa_dims* d, int64_t window, int64_t n_si
   a.seq_lens = cache->seq_lens;
   a.table_stride = cache->table_stride;
   a.n_pages = cache->n_pages;
-  a.cap = d->n_kv;
+  a.cap = (int32_t)d->n_kv;
   a.page_size = cache->page_size;
+  while ((1 << a.page_shift) < a.page_size) ++a.page_shift;
   a.batch = (int32_t)d->batch;
   a.G = d->h_kv;
   a.R = d->h_q / d->h_kv;
-  a.window = window;
-  a.sink = msa::min64(n_sink, d->n_kv);
+  a.window = window == 0 ? a.cap : (int32_t)msa::min64(window, d->n_kv);
+  a.sink = (int32_t)msa::min64(n_sink, d->n_kv);
   a.scale = d->scale;
   a.out = reinterpret_cast<__nv_bfloat16*>(out);
   a.lse = lse;
