@@ -8,21 +8,29 @@
 // shared by the R heads of a group and come from L2) together with the
 // exponentials: a 128 x 128 tile costs 1024 clocks of MMA and 1024 of ex2.
 // Design: persistent, one CTA per SM, warp-specialised:
-//   warps 0-3, 4-7  softmax of row tile A / B: thread = row; S from TMEM, one
-//                   running (m, l) per row, P = bf16(2^{s - m}) back into the
-//                   first 64 columns of S, the A operand of O += P V
+//   warps 0-3, 4-7  softmax halves A and B: thread = row; S from TMEM into
+//                   registers, one running (m, l) per row, P = bf16(2^{s - m}) into
+//                   TMEM, the A operand of O += P V
 //   warp 8          TMA: the item's Q tiles, then K and V tiles through a ring
+//   warp 9          MMA
 //   warps 10, 11    idle (they fill the control warpgroup)
-//   warp 9          MMA: S_X = Q_X K^T, O_X += P_X V for X = A, B in turn, so that
-//                   one tile's softmax runs under the other's products
 // A row tile is 128 / R tokens x the R heads of a group, so that a short window
 // is covered by few key tiles (W + 128 / R keys instead of W + 128) and the
-// heads share K and V; an item is two adjacent row tiles.  Key tiles start at
-// the first key the item's window reaches (TMA rows need no alignment).
+// heads share K and V.  An item is two adjacent row tiles, one per half -- or,
+// when that would leave SMs without work, one row tile whose key tiles the halves
+// take in turn, each with its own (m, l, O), joined at the end.  Key tiles start
+// at the first key the item's window reaches (TMA rows need no alignment).
+// TMEM: one S buffer (128 columns) that the halves use in turn, P_A, P_B (64 each),
+// O_A, O_B (128 each).  S is free again as soon as it is in registers, so the MMA
+// warp runs S three (tile, half) steps ahead of P V: S0 S1 S2 PV0 S3 PV1 S4 ..., and
+// neither half waits for a product of its own (with P in S's columns, S(j + 1)
+// had to wait for P V(j): 2800 clocks a tile instead of the rate below).
 // The running maximum is kept until a row exceeds it by 2^8: then O is
-// rescaled by the softmax warps themselves, between S(j) and P(j), while no
-// product of that tile is in flight.  Exact: P and l use the same maximum.
+// rescaled by the softmax warps themselves, after P V of the tile before.
+// Exact: P and l use the same maximum.
 // P is rounded to bf16 (2^-9 relative a weight) for the product; l sums fp32.
+#include <type_traits>
+
 #include "common.cuh"
 #include "layer_args.cuh"
 #include "window_tiles.cuh"
@@ -38,12 +46,15 @@ constexpr int kWaRegsAtLaunch = 168, kWaRegsControl = 104, kWaRegsSoftmax = 200;
 static_assert(kWaRegsControl + 2 * kWaRegsSoftmax == 3 * kWaRegsAtLaunch,
               "warpgroup register shares must add up to the launch allocation");
 constexpr int kWaRing = 5;                              // 32 KB K or V tiles in flight
+constexpr int kWaAhead = 3;                             // steps S runs ahead of P V
 constexpr int kWaOffQ = 0;                              // Q_A, Q_B
 constexpr int kWaOffRing = 65536;
-constexpr int kWaOffBar = kWaOffRing + kWaRing * 32768;
+constexpr int kWaOffML = kWaOffRing + kWaRing * 32768;  // m, l of half B's rows
+constexpr int kWaOffBar = kWaOffML + 1024;
 enum {
   WB_Q_FULL = 0, WB_Q_EMPTY = 2, WB_S_FULL = 4, WB_P_FULL = 6, WB_PV_DONE = 8, WB_O_EMPTY = 10,
-  WB_KV_FULL = 12, WB_KV_EMPTY = 12 + kWaRing, WB_DRAIN = 12 + 2 * kWaRing, WB_COUNT
+  WB_S_READ = 12, WB_JOIN, WB_KV_FULL, WB_KV_EMPTY = WB_KV_FULL + kWaRing,
+  WB_DRAIN = WB_KV_EMPTY + kWaRing, WB_COUNT
 };
 constexpr int kWaOffMisc = kWaOffBar + WB_COUNT * 8;
 constexpr int kWaSmemBytes = 1024 + kWaOffMisc + 16;
@@ -56,7 +67,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
                            const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ WindowArgs a, int32_t tiles_per_item,
-                           int64_t n_items) {
+                           int32_t n_items) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -71,14 +82,16 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       mbar_init(bar + WB_Q_FULL + x, 1);
       mbar_init(bar + WB_Q_EMPTY + x, 1);
       mbar_init(bar + WB_S_FULL + x, 1);
-      mbar_init(bar + WB_P_FULL + x, 128);
+      mbar_init(bar + WB_P_FULL + x, 4);           // a lane of each warp
       mbar_init(bar + WB_PV_DONE + x, 1);
-      mbar_init(bar + WB_O_EMPTY + x, 128);
+      mbar_init(bar + WB_O_EMPTY + x, 4);
     }
     for (int s = 0; s < kWaRing; ++s) {
       mbar_init(bar + WB_KV_FULL + s, 1);
       mbar_init(bar + WB_KV_EMPTY + s, 1);
     }
+    mbar_init(bar + WB_S_READ, 4);
+    mbar_init(bar + WB_JOIN, 4);
     mbar_init(bar + WB_DRAIN, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -90,13 +103,29 @@ __global__ void __launch_bounds__(kWaThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;          // S_A, S_B, O_A, O_B: 128 columns each
+  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t kColP = 128, kColO = 256;         // S at 0; P_A, P_B; O_A, O_B
   // k-th completion of a barrier has parity k & 1; the whole warp decides together
-  auto W = [&](int id, int64_t k) {
-    return __all_sync(0xffffffffu,
-                      mbar_wait(bar + id, (uint32_t)(k & 1), abort_flag, err));
+  auto W = [&](int id, uint32_t k) {
+    return __all_sync(0xffffffffu, mbar_wait(bar + id, k & 1u, abort_flag, err));
   };
+  auto arrive = [&](int id) {                          // for the whole warp
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar + id);
+  };
+  const bool split = tiles_per_item == 1;              // the halves share one row tile
   WinItem it{};
+  // step i of an item is key tile tile_of(i) of half i & 1; does the half need it?
+  auto n_steps = [&]() { return split ? it.nt : 2 * it.nt; };
+  auto tile_of = [&](int i) { return split ? i : i >> 1; };
+  auto takes = [&](int i) {
+    if (split) return i < it.nt;
+    const int j = i >> 1;
+    return (i & 1) ? it.rows[1] && j < it.nt && (j < it.ns || j >= it.beg_b) : j <= it.end_a;
+  };
+  // ring slots of an item's tiles, in the order K0 K1 V0 K2 V1 ... (counted from its first)
+  auto slot_k = [&](int j) { return (uint32_t)(j == 0 ? 0 : 2 * j - 1); };
+  auto slot_v = [&](int j) { return (uint32_t)(j == it.nt - 1 ? 2 * j + 1 : 2 * j + 2); };
 
   if (warp >= 8) {
     setmaxnreg_dec<kWaRegsControl>();
@@ -107,10 +136,10 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       prefetch_tensormap(&tm_k);
       prefetch_tensormap(&tm_v);
     }
-    int64_t nq[2] = {0, 0}, n = 0;           // Q loads per tile, ring slots
+    uint32_t nq[2] = {0, 0}, n = 0;          // Q loads per tile, ring slots
     bool ok = true;
     auto push = [&](const CUtensorMap* tm, int32_t key0) {
-      const int s = (int)(n % kWaRing);
+      const uint32_t s = n % kWaRing;
       if (n >= kWaRing && !W(WB_KV_EMPTY + s, n / kWaRing - 1)) return false;
       if (lane == 0) {
         uint8_t* dst = base + kWaOffRing + s * 32768;
@@ -121,7 +150,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       ++n;
       return true;
     };
-    for (int64_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+    for (int32_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
       win_item(it, a, i, tiles_per_item);
       for (int x = 0; ok && x < 2; ++x) {
         if (!it.rows[x]) continue;
@@ -135,110 +164,111 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         }
         if (ok) ++nq[x];
       }
+      if (ok && it.nt > 0) ok = push(&tm_k, win_key0(it, 0));
       for (int j = 0; ok && j < it.nt; ++j)
-        ok = push(&tm_k, win_key0(it, j)) && push(&tm_v, win_key0(it, j));
+        ok = (j + 1 == it.nt || push(&tm_k, win_key0(it, j + 1))) && push(&tm_v, win_key0(it, j));
     }
     // no copy may still be writing shared memory when the block exits
     if (lane == 0) {
-      for (int64_t k = n > kWaRing ? n - kWaRing : 0; k < n; ++k)
-        mbar_drain(bar + WB_KV_FULL + k % kWaRing, (uint32_t)((k / kWaRing) & 1), err);
+      for (uint32_t k = n > kWaRing ? n - kWaRing : 0; k < n; ++k)
+        mbar_drain(bar + WB_KV_FULL + k % kWaRing, (k / kWaRing) & 1u, err);
       for (int x = 0; x < 2; ++x)
-        if (nq[x] > 0) mbar_drain(bar + WB_Q_FULL + x, (uint32_t)((nq[x] - 1) & 1), err);
+        if (nq[x] > 0) mbar_drain(bar + WB_Q_FULL + x, (nq[x] - 1) & 1u, err);
     }
   } else if (warp == 9) {
     // ---------------- MMA ----------------
     constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, 0), kIdO = idesc_bf16_f32(128, 128, 1);
-    int64_t nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0}, n = 0;
+    // completions so far: Q tiles used, S products, P V products, items with an O
+    uint32_t nq[2] = {0, 0}, ns = 0, np[2] = {0, 0}, no[2] = {0, 0}, n0 = 0;
     bool ok = true;
-    for (int64_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+    for (int32_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
       win_item(it, a, i, tiles_per_item);
-      int last[2], pend[2] = {-1, -1};       // last key tile of X; tile whose P V is due
-      bool begun[2] = {false, false};
-      for (int x = 0; x < 2; ++x) {
-        last[x] = -1;
-        for (int j = it.nt - 1; j >= 0 && last[x] < 0; --j)
-          if (win_need(it, a, x, j)) last[x] = j;
-      }
-      const int64_t n0 = n;
-      auto slot_k = [&](int j) { return n0 + 2 * j; };
-      auto slot_v = [&](int j) { return n0 + 2 * j + 1; };
-      // O_X (+)= P_X V(j)
-      auto pv = [&](int x, int j) {
-        if (!W(WB_P_FULL + x, np[x])) return false;
-        if (!begun[x] && no[x] > 0 && !W(WB_O_EMPTY + x, no[x] - 1)) return false;
-        const int64_t sv = slot_v(j);
-        if (!W(WB_KV_FULL + (int)(sv % kWaRing), sv / kWaRing)) return false;
-        const uint32_t va = smem_u32(base + kWaOffRing + (int)(sv % kWaRing) * 32768);
+      bool begun[2] = {false, false}, seen_q[2] = {false, false};
+      const int n_st = n_steps();
+      int left = 0;                          // S products still to come
+      for (int k = 0; k < n_st; ++k) left += takes(k) ? 1 : 0;
+      // S = Q_x K(j)^T of step k, once the buffer's last S is in registers
+      auto issue_s = [&](auto half, int k) {
+        constexpr int x = decltype(half)::value;
+        if (!ok || k >= n_st || !takes(k)) return;
+        const int j = tile_of(k);
+        const uint32_t sk = n0 + slot_k(j), slot = sk % kWaRing;
+        const bool first = split || x == 0 || !takes(k - 1);
+        if (first && !W(WB_KV_FULL + slot, sk / kWaRing)) { ok = false; return; }
+        if (!seen_q[x] && (!split || x == 0) && !W(WB_Q_FULL + x, nq[x])) { ok = false; return; }
+        seen_q[x] = true;
+        if (ns > 0 && !W(WB_S_READ, ns - 1)) { ok = false; return; }
+        ++ns;
+        --left;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
+          const uint32_t ka = smem_u32(base + kWaOffRing + slot * 32768);
+          const uint32_t qa = smem_u32(base + kWaOffQ + (split ? 0 : x) * 32768);
+          const uint64_t qd = smem_desc_sw128(qa, 16, 1024), kd = smem_desc_sw128(ka, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {      // the start address counts 16-byte units
+            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) / 16;
+            umma_bf16(tmem, qd + off, kd + off, kIdS, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(bar + WB_S_FULL + x);
+          if (split || x == 1 || !takes(k + 1)) umma_commit(bar + WB_KV_EMPTY + slot);
+          if (left == 0) {
+            umma_commit(bar + WB_Q_EMPTY);
+            if (it.rows[1]) umma_commit(bar + WB_Q_EMPTY + 1);
+          }
+        }
+        __syncwarp();
+      };
+      // O_x (+)= P_x V(j) of step k
+      auto issue_pv = [&](auto half, int k) {
+        constexpr int x = decltype(half)::value;
+        if (!ok || k >= n_st || !takes(k)) return;
+        const int j = tile_of(k);
+        const uint32_t sv = n0 + slot_v(j), slot = sv % kWaRing;
+        uint8_t* tile = base + kWaOffRing + slot * 32768;
+        if (split || x == 0 || !takes(k - 1)) {          // the tile's first use
+          if (!W(WB_KV_FULL + slot, sv / kWaRing)) { ok = false; return; }
+          // keys past the sequence's end may hold anything: their V rows are cleared
+          // (P is 0 there, and 0 * NaN would not be)
+          const int32_t k0 = win_key0(it, j);
+          if (it.len < a.n_kv && k0 + 128 > it.len) win_clear_rows(tile, it.len - k0, lane);
+        }
+        if (!begun[x] && no[x] > 0 && !W(WB_O_EMPTY + x, no[x] - 1)) { ok = false; return; }
+        if (!W(WB_P_FULL + x, np[x])) { ok = false; return; }
+        ++np[x];
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t vd = smem_desc_sw128(smem_u32(tile), 16384, 1024);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + kk * 8,
-                         smem_desc_sw128(va + kk * 2048, 16384, 1024), kIdO,
-                         begun[x] || kk > 0 ? 1u : 0u);
+            umma_bf16_ts(tmem + kColO + 128 * x, tmem + kColP + 64 * x + kk * 8,
+                         vd + kk * (2048 / 16), kIdO, begun[x] || kk > 0 ? 1u : 0u);
           umma_commit(bar + WB_PV_DONE + x);
+          if (split || x == 1 || !takes(k + 1)) umma_commit(bar + WB_KV_EMPTY + slot);
         }
         __syncwarp();
         begun[x] = true;
-        ++np[x];
-        return true;
       };
-      for (int j = 0; ok && j <= it.nt; ++j) {
-        if (j < it.nt) {
-          const int64_t sk = slot_k(j);
-          ok = W(WB_KV_FULL + (int)(sk % kWaRing), sk / kWaRing);
-          if (!ok) break;
-          // keys past the sequence's end may hold anything: their V rows are
-          // cleared (P is 0 there, and 0 * NaN would not be)
-          const int32_t k0 = win_key0(it, j);
-          if (it.len < a.n_kv && k0 + 128 > it.len) {
-            const int64_t sv = slot_v(j);
-            ok = W(WB_KV_FULL + (int)(sv % kWaRing), sv / kWaRing);
-            if (!ok) break;
-            win_clear_rows(base + kWaOffRing + (int)(sv % kWaRing) * 32768, it.len - k0, lane);
-          }
-        }
-        for (int x = 0; ok && x < 2; ++x) {
-          if (pend[x] >= 0) {
-            ok = pv(x, pend[x]);
-            pend[x] = -1;
-          }
-          if (!ok || j >= it.nt || !win_need(it, a, x, j)) continue;
-          // S_X overwrites the columns P_X was read from
-          if (np[x] > 0 && !W(WB_PV_DONE + x, np[x] - 1)) { ok = false; break; }
-          if (!begun[x] && !W(WB_Q_FULL + x, nq[x])) { ok = false; break; }
-          tc_fence_after();
-          if (lane == 0) {
-            const int64_t sk = slot_k(j);
-            const uint32_t ka = smem_u32(base + kWaOffRing + (int)(sk % kWaRing) * 32768);
-            const uint32_t qa = smem_u32(base + kWaOffQ + x * 32768);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-              umma_bf16(tmem + 128 * x, smem_desc_sw128(qa + off, 16, 1024),
-                        smem_desc_sw128(ka + off, 16, 1024), kIdS, kk > 0 ? 1u : 0u);
-            }
-            umma_commit(bar + WB_S_FULL + x);
-            if (j == last[x]) umma_commit(bar + WB_Q_EMPTY + x);
-          }
-          __syncwarp();
-          pend[x] = j;
-        }
-        // K(j) is free after this step's S, V(j - 1) after its P V
-        if (ok && lane == 0) {
-          if (j < it.nt) umma_commit(bar + WB_KV_EMPTY + (int)(slot_k(j) % kWaRing));
-          if (j > 0) umma_commit(bar + WB_KV_EMPTY + (int)(slot_v(j - 1) % kWaRing));
-        }
-        __syncwarp();
+      using A = std::integral_constant<int, 0>;
+      using B = std::integral_constant<int, 1>;
+      static_assert(kWaAhead == 3, "the order below");
+      issue_s(A{}, 0);
+      issue_s(B{}, 1);
+      issue_s(A{}, 2);
+      for (int k = 0; ok && k < n_st; k += 2) {
+        issue_pv(A{}, k);
+        issue_s(B{}, k + 3);
+        issue_pv(B{}, k + 1);
+        issue_s(A{}, k + 4);
       }
-      n = n0 + 2 * (int64_t)it.nt;
+      n0 += 2 * (uint32_t)it.nt;
       for (int x = 0; x < 2; ++x) {
         if (it.rows[x]) ++nq[x];
-        if (last[x] >= 0) ++no[x];
+        if (begun[x]) ++no[x];
       }
     }
     // every MMA issued has finished before the tensor memory is freed
-    if (lane == 0) {
+    if (elect_one()) {
       umma_commit(bar + WB_DRAIN);
       mbar_drain(bar + WB_DRAIN, 0, err);
     }
@@ -246,26 +276,29 @@ __global__ void __launch_bounds__(kWaThreads, 1)
   }
   } else {
     setmaxnreg_inc<kWaRegsSoftmax>();
-    // ---------------- softmax of row tile x; thread = row ----------------
+    // ---------------- softmax of half x; thread = row ----------------
     const int x = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t ts = tmem + lane_base + 128 * x, to = ts + 256;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t tp = lanes + kColP + 64 * x, to = lanes + kColO + 128 * x;
     const float scale_log2 = a.scale * 1.4426950408889634f;
     const uint64_t scale2 = pack_f32x2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
     const int32_t tpt = 128 / a.R;            // tokens per row tile
-    int64_t ns = 0, np = 0;
+    float2* ml_b = reinterpret_cast<float2*>(base + kWaOffML);
+    uint32_t ns = 0, np = 0, np_other = 0, nj = 0;
     bool ok = true;
-    for (int64_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+    for (int32_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
       win_item(it, a, i, tiles_per_item);
-      const int32_t i_row = it.i0 + x * tpt + row / a.R;         // query index
+      const int32_t first = it.i0 + (split ? 0 : x * tpt);       // the row tile's first query
+      const int32_t i_row = first + row / a.R;
       const int32_t t = it.q_pos0 + i_row;
-      const int32_t i_w0 = it.i0 + x * tpt + (quarter * 32) / a.R;
-      const int32_t t_min = it.q_pos0 + i_w0, t_max = t_min + (31 / a.R);
+      const int32_t t_min = it.q_pos0 + first + (quarter * 32) / a.R, t_max = t_min + (31 / a.R);
       float m = -INFINITY, l = 0.f;
       bool begun = false;
-      for (int j = 0; j < it.nt; ++j) {
-        if (!win_need(it, a, x, j)) continue;
+      const int n_st = n_steps();
+      for (int k = x; k < n_st; k += 2) {
+        if (!takes(k)) continue;
+        const int j = tile_of(k);
         if (!W(WB_S_FULL + x, ns)) { ok = false; break; }
         ++ns;
         tc_fence_after();
@@ -273,8 +306,10 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         uint32_t s[128];
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc)
-          tmem_ld_32x32b_x32(ts + 32 * cc, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * cc));
+          tmem_ld_32x32b_x32(lanes + 32 * cc, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * cc));
         tmem_ld_wait();
+        tc_fence_before();
+        arrive(WB_S_READ);
         // visible columns c: c <= hi and (c >= lo or c < sk)
         int32_t hi, lo, sk;
         bool full;
@@ -294,17 +329,25 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           for (int c = 0; c < 128; ++c)
             if (!(c <= hi && (c >= lo || c < sk))) s[c] = 0xFF800000u;   // -inf
         }
-        float mx = u2f(s[0]);
+        float mq[4];                          // four chains: the latency of one is 64 steps
 #pragma unroll
-        for (int c = 1; c < 127; c += 2) mx = fmax3f(mx, u2f(s[c]), u2f(s[c + 1]));
-        mx = fmaxf(mx, u2f(s[127])) * scale_log2;
+        for (int q = 0; q < 4; ++q) {
+          mq[q] = fmaxf(u2f(s[32 * q]), u2f(s[32 * q + 1]));
+#pragma unroll
+          for (int c = 2; c < 32; c += 2)
+            mq[q] = fmax3f(mq[q], u2f(s[32 * q + c]), u2f(s[32 * q + c + 1]));
+        }
+        const float mx = fmaxf(fmax3f(mq[0], mq[1], mq[2]), mq[3]) * scale_log2;
         const bool grow = mx > m + kLazyLog2 || (m == -INFINITY && mx > -INFINITY);
+        // P V of this half's tile before: P and O are free
+        if (begun && !W(WB_PV_DONE + x, np - 1)) { ok = false; break; }
         if (__any_sync(0xffffffffu, grow)) {
           const float mn = grow ? mx : m;
           const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
           l *= f;
           m = mn;
           if (begun) {
+            tc_fence_after();
             const uint64_t f2 = pack_f32x2(__float_as_uint(f), __float_as_uint(f));
 #pragma unroll 1
             for (int cc = 0; cc < 8; ++cc) {
@@ -338,55 +381,79 @@ __global__ void __launch_bounds__(kWaThreads, 1)
             l2[q & 1] = add_f32x2(l2[q & 1], pack_f32x2(__float_as_uint(u), __float_as_uint(v)));
             pk[q] = pack_bf16x2(u, v);
           }
-          tmem_st_32x32b_x16(ts + 16 * cc, pk);
+          tmem_st_32x32b_x16(tp + 16 * cc, pk);
         }
         float u, v;
         unpack_f32x2(add_f32x2(l2[0], l2[1]), u, v);
         l += u + v;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar + WB_P_FULL + x);
+        arrive(WB_P_FULL + x);
         begun = true;
         ++np;
       }
       if (!ok) break;
-      // the item's rows leave: o = O / l
-      const bool store = i_row < a.n_q && x < tiles_per_item;
-      const bool live = store && t < it.len && begun;
-      const int64_t orow =
-          ((int64_t)it.b * a.n_q + i_row) * ((int64_t)a.G * a.R) + (int64_t)it.g * a.R + row % a.R;
       if (begun) {
         if (!W(WB_PV_DONE + x, np - 1)) { ok = false; break; }
         tc_fence_after();
       }
+      // shared row tile with two key tiles or more: half B hands over its (m, l), half A
+      // reads B's accumulators from the same TMEM lanes
+      float fa = 1.f, fb = 0.f;
+      bool both = false;
+      if (split && it.nt > 1) {
+        if (x == 1) {
+          ml_b[row] = make_float2(m, l);
+          arrive(WB_JOIN);
+          continue;                            // A frees B's accumulators
+        }
+        if (!W(WB_JOIN, nj)) { ok = false; break; }
+        ++nj;
+        np_other += it.nt >> 1;                // half B's products: every second tile
+        if (!W(WB_PV_DONE + 1, np_other - 1)) { ok = false; break; }
+        tc_fence_after();
+        const float2 o = ml_b[row];
+        const float mm = fmaxf(m, o.x), z = mm == -INFINITY ? 0.f : mm;
+        fa = ex2_approx(m - z);
+        fb = ex2_approx(o.x - z);
+        l = l * fa + o.y * fb;
+        m = mm;
+        both = true;
+      }
+      // the item's rows leave: o = O / l
+      const bool store = i_row < a.n_q && !(split && x == 1);
+      const bool live = store && t < it.len && begun;
+      const int64_t orow =
+          ((int64_t)it.b * a.n_q + i_row) * ((int64_t)a.G * a.R) + (int64_t)it.g * a.R + row % a.R;
       const float inv = live && l != 0.f ? 1.f / l : 0.f;
+      fa *= inv;
+      fb *= inv;
       if (store) a.lse[orow] = live ? m * 0.6931471805599453f + logf(l) : -INFINITY;
 #pragma unroll 1
-      for (int cc = 0; cc < 4; ++cc) {
-        uint32_t r[32];
-        if (begun) {
-          tmem_ld_32x32b_x32(to + 32 * cc, r);
-          tmem_ld_wait();
-        }
+      for (int cc = 0; cc < 8; ++cc) {
+        uint32_t r[16], rb[16];
+        if (begun) tmem_ld_32x32b_x16(to + 16 * cc, r);
+        if (both) tmem_ld_32x32b_x16(to + 128 + 16 * cc, rb);
+        tmem_ld_wait();
         if (store) {
-          __nv_bfloat16* dst = a.out + orow * kHeadDim + 32 * cc;
+          uint32_t pk[8];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              pk[q] = live ? pack_bf16x2(u2f(r[16 * h + 2 * q]) * inv,
-                                         u2f(r[16 * h + 2 * q + 1]) * inv)
-                           : 0u;
-            st_global_v8(reinterpret_cast<float*>(dst + 16 * h), u2f(pk[0]), u2f(pk[1]),
-                         u2f(pk[2]), u2f(pk[3]), u2f(pk[4]), u2f(pk[5]), u2f(pk[6]), u2f(pk[7]));
+          for (int q = 0; q < 8; ++q) {
+            float u = live ? u2f(r[2 * q]) * fa : 0.f, v = live ? u2f(r[2 * q + 1]) * fa : 0.f;
+            if (both && live) {
+              u += u2f(rb[2 * q]) * fb;
+              v += u2f(rb[2 * q + 1]) * fb;
+            }
+            pk[q] = pack_bf16x2(u, v);
           }
+          st_global_v8(reinterpret_cast<float*>(a.out + orow * kHeadDim + 16 * cc), u2f(pk[0]),
+                       u2f(pk[1]), u2f(pk[2]), u2f(pk[3]), u2f(pk[4]), u2f(pk[5]), u2f(pk[6]),
+                       u2f(pk[7]));
         }
       }
-      if (begun) {
-        tc_fence_before();
-        mbar_arrive(bar + WB_O_EMPTY + x);
-      }
+      tc_fence_before();
+      if (begun) arrive(WB_O_EMPTY + x);
+      if (both) arrive(WB_O_EMPTY + 1);
     }
   }
   tc_fence_before();
@@ -408,8 +475,9 @@ cudaError_t launch_window_attn_fwd(const CUtensorMap& tm_q, const CUtensorMap& t
   int32_t per = 2;
   if (a.batch * a.G * ((tiles + 1) / 2) < sms) per = 1;
   const int64_t items = a.batch * a.G * ((tiles + per - 1) / per);
+  if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
   window_attn_fwd_kernel<<<(unsigned)min64(items, sms), kWaThreads, kWaSmemBytes, st>>>(
-      tm_q, tm_k, tm_v, a, per, items);
+      tm_q, tm_k, tm_v, a, per, (int32_t)items);
   return cudaGetLastError();
 }
 

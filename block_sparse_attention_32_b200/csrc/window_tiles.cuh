@@ -7,6 +7,19 @@
 
 namespace msa {
 
+// one thread of the warp, always the same, in a form that lets the compiler keep
+// what the branch computes in uniform registers (tcgen05.mma takes its operands
+// from there)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
 // An item: one or two adjacent row tiles (128 / R queries x R heads each) of
 // one (batch, group), and its key tiles: `ns` tiles of sinks [0, s_end) that lie
 // before the window, then tiles of 128 keys from `wlo` on.
@@ -14,6 +27,7 @@ struct WinItem {
   int32_t b, g, i0;          // first query of row tile A
   int32_t q_pos0, W, len;    // len: min(kv_len[b], n_kv)
   int32_t wlo, s_end, ns, nt;
+  int32_t end_a, beg_b;      // last key tile that A sees; first behind the sinks that B sees
   bool rows[2];              // row tile X has a query below n_q and len
   int32_t x0[2], x1[2];      // positions of its first and last such query
 };
@@ -54,16 +68,13 @@ __device__ __forceinline__ void win_item(WinItem& it, const WindowArgs& a, int64
   it.s_end = (int32_t)min64(a.sink, it.wlo);
   it.ns = thi < 0 ? 0 : (it.s_end + 127) / 128;
   it.nt = thi < 0 ? 0 : it.ns + (thi + 1 - it.wlo + 127) / 128;
+  it.end_a = it.rows[0] ? it.ns + (it.x1[0] - it.wlo) / 128 : -1;
+  // (sinks that reach past wlo are visible to B from the first tile on)
+  it.beg_b = it.rows[1] && a.sink <= it.wlo ? it.ns + max(0, it.x0[1] - it.W + 1 - it.wlo) / 128
+                                            : it.ns;
 }
 __device__ __forceinline__ int32_t win_key0(const WinItem& it, int j) {
   return j < it.ns ? 128 * j : it.wlo + 128 * (j - it.ns);
-}
-// does row tile x see any key of tile j?
-__device__ __forceinline__ bool win_need(const WinItem& it, const WindowArgs& a, int x, int j) {
-  if (!it.rows[x]) return false;
-  if (j < it.ns) return true;
-  const int32_t k0 = win_key0(it, j);
-  return k0 <= it.x1[x] && (k0 + 127 > it.x0[x] - it.W || k0 < a.sink);
 }
 
 // zeroes rows r0 .. 127 of a 128 x 128 bf16 tile (two 64-column panels), by a warp
