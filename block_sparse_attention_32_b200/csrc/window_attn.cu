@@ -12,8 +12,8 @@
 //                   registers, one running (m, l) per row, P = bf16(2^{s - m}) into
 //                   TMEM, the A operand of O += P V
 //   warp 8          TMA: the item's Q tiles, then K and V tiles through a ring
-//   warp 9          MMA
-//   warps 10, 11    idle (they fill the control warpgroup)
+//   warp 9          issues S = Q K^T;  warp 10  issues O += P V
+//   warp 11         idle (it fills the control warpgroup)
 // A row tile is 128 / R tokens x the R heads of a group, so that a short window
 // is covered by few key tiles (W + 128 / R keys instead of W + 128) and the
 // heads share K and V.  An item is two adjacent row tiles, one per half -- or,
@@ -21,10 +21,11 @@
 // take in turn, each with its own (m, l, O), joined at the end.  Key tiles start
 // at the first key the item's window reaches (TMA rows need no alignment).
 // TMEM: one S buffer (128 columns) that the halves use in turn, P_A, P_B (64 each),
-// O_A, O_B (128 each).  S is free again as soon as it is in registers, so the MMA
-// warp runs S three (tile, half) steps ahead of P V: S0 S1 S2 PV0 S3 PV1 S4 ..., and
-// neither half waits for a product of its own (with P in S's columns, S(j + 1)
-// had to wait for P V(j): 2800 clocks a tile instead of the rate below).
+// O_A, O_B (128 each).  S is free again as soon as it is in registers, so neither
+// half waits for a product of its own: the next S is made while a half is at its
+// exponentials.  (With P in S's columns, S(j + 1) had to wait for P V(j): 2800
+// clocks a tile; with one warp issuing both products, 2300: the issue of eight MMAs
+// takes as long as they do, and the waits between came on top.)
 // The running maximum is kept until a row exceeds it by 2^8: then O is
 // rescaled by the softmax warps themselves, after P V of the tile before.
 // Exact: P and l use the same maximum.
@@ -42,11 +43,10 @@ constexpr int kWaThreads = 384;
 // registers per thread: 168 at launch (65536 / 384 rounded down to the allocation
 // unit; the launcher checks the compiled count); the control warpgroup gives
 // some to the two softmax warpgroups, whose S row alone takes 128
-constexpr int kWaRegsAtLaunch = 168, kWaRegsControl = 104, kWaRegsSoftmax = 200;
+constexpr int kWaRegsAtLaunch = 168, kWaRegsControl = 72, kWaRegsSoftmax = 216;
 static_assert(kWaRegsControl + 2 * kWaRegsSoftmax == 3 * kWaRegsAtLaunch,
               "warpgroup register shares must add up to the launch allocation");
 constexpr int kWaRing = 5;                              // 32 KB K or V tiles in flight
-constexpr int kWaAhead = 3;                             // steps S runs ahead of P V
 constexpr int kWaOffQ = 0;                              // Q_A, Q_B
 constexpr int kWaOffRing = 65536;
 constexpr int kWaOffML = kWaOffRing + kWaRing * 32768;  // m, l of half B's rows
@@ -54,7 +54,7 @@ constexpr int kWaOffBar = kWaOffML + 1024;
 enum {
   WB_Q_FULL = 0, WB_Q_EMPTY = 2, WB_S_FULL = 4, WB_P_FULL = 6, WB_PV_DONE = 8, WB_O_EMPTY = 10,
   WB_S_READ = 12, WB_JOIN, WB_KV_FULL, WB_KV_EMPTY = WB_KV_FULL + kWaRing,
-  WB_DRAIN = WB_KV_EMPTY + kWaRing, WB_COUNT
+  WB_DRAIN = WB_KV_EMPTY + kWaRing, WB_COUNT = WB_DRAIN + 2
 };
 constexpr int kWaOffMisc = kWaOffBar + WB_COUNT * 8;
 constexpr int kWaSmemBytes = 1024 + kWaOffMisc + 16;
@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     mbar_init(bar + WB_S_READ, 4);
     mbar_init(bar + WB_JOIN, 4);
     mbar_init(bar + WB_DRAIN, 1);
+    mbar_init(bar + WB_DRAIN + 1, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -176,25 +177,24 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         if (nq[x] > 0) mbar_drain(bar + WB_Q_FULL + x, (nq[x] - 1) & 1u, err);
     }
   } else if (warp == 9) {
-    // ---------------- MMA ----------------
-    constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, 0), kIdO = idesc_bf16_f32(128, 128, 1);
-    // completions so far: Q tiles used, S products, P V products, items with an O
-    uint32_t nq[2] = {0, 0}, ns = 0, np[2] = {0, 0}, no[2] = {0, 0}, n0 = 0;
+    // ---------------- S = Q K^T ----------------
+    constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, 0);
+    const uint32_t ring = smem_u32(base + kWaOffRing), qs = smem_u32(base + kWaOffQ);
+    uint32_t nq[2] = {0, 0}, ns = 0, n0 = 0;     // Q tiles used, S products, ring slots
     bool ok = true;
     for (int32_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
       win_item(it, a, i, tiles_per_item);
-      bool begun[2] = {false, false}, seen_q[2] = {false, false};
+      bool seen_q[2] = {false, false};
       const int n_st = n_steps();
-      int left = 0;                          // S products still to come
+      int left = 0;                          // products still to come
       for (int k = 0; k < n_st; ++k) left += takes(k) ? 1 : 0;
-      // S = Q_x K(j)^T of step k, once the buffer's last S is in registers
-      auto issue_s = [&](auto half, int k) {
+      // step k (of half x), once the buffer's last S is in registers
+      auto issue = [&](auto half, int k) {
         constexpr int x = decltype(half)::value;
         if (!ok || k >= n_st || !takes(k)) return;
-        const int j = tile_of(k);
-        const uint32_t sk = n0 + slot_k(j), slot = sk % kWaRing;
-        const bool first = split || x == 0 || !takes(k - 1);
-        if (first && !W(WB_KV_FULL + slot, sk / kWaRing)) { ok = false; return; }
+        const uint32_t sk = n0 + slot_k(tile_of(k)), slot = sk % kWaRing;
+        if (split || x == 0 || !takes(k - 1))
+          if (!W(WB_KV_FULL + slot, sk / kWaRing)) { ok = false; return; }
         if (!seen_q[x] && (!split || x == 0) && !W(WB_Q_FULL + x, nq[x])) { ok = false; return; }
         seen_q[x] = true;
         if (ns > 0 && !W(WB_S_READ, ns - 1)) { ok = false; return; }
@@ -202,9 +202,8 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         --left;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t ka = smem_u32(base + kWaOffRing + slot * 32768);
-          const uint32_t qa = smem_u32(base + kWaOffQ + (split ? 0 : x) * 32768);
-          const uint64_t qd = smem_desc_sw128(qa, 16, 1024), kd = smem_desc_sw128(ka, 16, 1024);
+          const uint64_t qd = smem_desc_sw128(qs + (split ? 0 : x) * 32768, 16, 1024);
+          const uint64_t kd = smem_desc_sw128(ring + slot * 32768, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {      // the start address counts 16-byte units
             const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) / 16;
@@ -219,8 +218,30 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         }
         __syncwarp();
       };
-      // O_x (+)= P_x V(j) of step k
-      auto issue_pv = [&](auto half, int k) {
+      for (int k = 0; ok && k < n_st; k += 2) {
+        issue(std::integral_constant<int, 0>{}, k);
+        issue(std::integral_constant<int, 1>{}, k + 1);
+      }
+      n0 += 2 * (uint32_t)it.nt;
+      for (int x = 0; x < 2; ++x)
+        if (it.rows[x]) ++nq[x];
+    }
+    // every MMA issued has finished before the tensor memory is freed
+    if (elect_one()) {
+      umma_commit(bar + WB_DRAIN);
+      mbar_drain(bar + WB_DRAIN, 0, err);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ---------------- O += P V ----------------
+    constexpr uint32_t kIdO = idesc_bf16_f32(128, 128, 1);
+    uint32_t np[2] = {0, 0}, no[2] = {0, 0}, n0 = 0;     // products, items with an O, ring slots
+    bool ok = true;
+    for (int32_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+      win_item(it, a, i, tiles_per_item);
+      bool begun[2] = {false, false};
+      const int n_st = n_steps();
+      auto issue = [&](auto half, int k) {
         constexpr int x = decltype(half)::value;
         if (!ok || k >= n_st || !takes(k)) return;
         const int j = tile_of(k);
@@ -249,28 +270,17 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         __syncwarp();
         begun[x] = true;
       };
-      using A = std::integral_constant<int, 0>;
-      using B = std::integral_constant<int, 1>;
-      static_assert(kWaAhead == 3, "the order below");
-      issue_s(A{}, 0);
-      issue_s(B{}, 1);
-      issue_s(A{}, 2);
       for (int k = 0; ok && k < n_st; k += 2) {
-        issue_pv(A{}, k);
-        issue_s(B{}, k + 3);
-        issue_pv(B{}, k + 1);
-        issue_s(A{}, k + 4);
+        issue(std::integral_constant<int, 0>{}, k);
+        issue(std::integral_constant<int, 1>{}, k + 1);
       }
       n0 += 2 * (uint32_t)it.nt;
-      for (int x = 0; x < 2; ++x) {
-        if (it.rows[x]) ++nq[x];
+      for (int x = 0; x < 2; ++x)
         if (begun[x]) ++no[x];
-      }
     }
-    // every MMA issued has finished before the tensor memory is freed
     if (elect_one()) {
-      umma_commit(bar + WB_DRAIN);
-      mbar_drain(bar + WB_DRAIN, 0, err);
+      umma_commit(bar + WB_DRAIN + 1);
+      mbar_drain(bar + WB_DRAIN + 1, 0, err);
     }
     __syncwarp();
   }
