@@ -19,13 +19,17 @@
 // items fill the tail that the long dk, dv items leave.  Which CTA takes an item
 // changes no result.
 //   warps 0-3, 4-7  P and dS: thread = accumulator row, columns 0-63 / 64-127
-//   warp 8          scheduler and TMA;  warp 9  MMA;  warp 10  -lse, -D of the
-//                   streamed rows;  warp 11 idle
+//   warp 8          scheduler and TMA;  warp 11  -lse, -D of the streamed rows
+//   warp 9          issues S and dP;  warp 10  issues dV and dK or dQ (the issue of
+//                   eight MMAs takes as long as they do: one warp for all of them
+//                   left the tensor core waiting)
 // TMEM: S (P in place, bf16), dP (dS in place), dV, dK or dQ: 128 columns each.
 // Per tile the tensor core runs dP(n), dV(n), S(n+1), dK(n): the exponentials of
 // n+1 run under dK(n) and dP(n+1), the dS of n under dV(n) and S(n+1).
 // A key block that many queries see (sinks; no window) is cut into chunks of
 // query tiles whose fp32 sums a last kernel adds in chunk order.
+#include <type_traits>
+
 #include "common.cuh"
 #include "layer_args.cuh"
 #include "window_tiles.cuh"
@@ -34,7 +38,7 @@ namespace msa {
 
 namespace {
 constexpr int kWbThreads = 384;
-constexpr int kWbRegsAtLaunch = 168, kWbRegsControl = 104, kWbRegsMath = 200;
+constexpr int kWbRegsAtLaunch = 168, kWbRegsControl = 88, kWbRegsMath = 208;
 static_assert(kWbRegsControl + 2 * kWbRegsMath == 3 * kWbRegsAtLaunch,
               "warpgroup register shares must add up to the launch allocation");
 constexpr int kWbOffStay = 0;                          // K, V or Q, dO: 32 KB each
@@ -44,12 +48,12 @@ constexpr int kWbOffBar = kWbOffMeta + 2 * 1024;
 enum {
   XB_ITEM_FULL = 0, XB_ITEM_EMPTY = 2, XB_STAY_FULL = 4, XB_STAY_EMPTY, XB_STR_FULL = 6,
   XB_STR_EMPTY = 8, XB_META_FULL = 10, XB_S_FULL = 12, XB_DP_FULL, XB_P_FULL, XB_DS_FULL, XB_DV_DONE, XB_DK_DONE,
-  XB_ACC_FULL, XB_ACC_EMPTY, XB_DRAIN, XB_COUNT
+  XB_ACC_FULL, XB_ACC_EMPTY, XB_DRAIN, XB_COUNT = XB_DRAIN + 2
 };
 constexpr int kWbOffMisc = kWbOffBar + XB_COUNT * 8;
 constexpr int kWbSmemBytes = 1024 + kWbOffMisc + 32;
 static_assert(kWbSmemBytes <= 232448, "shared memory per block");
-constexpr int kWbItemReaders = 10;     // warps that read an item's number: 0-7, 9, 10
+constexpr int kWbItemReaders = 11;     // warps that read an item's number: 0-7, 9-11
 constexpr int kWbMinChunk = 32;        // query tiles of a chunk at least
 constexpr int kWbSplit = 2 * 148;      // chunks aimed at when blocks are cut
 
@@ -264,13 +268,14 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     mbar_init(bar + XB_STAY_EMPTY, 1);
     mbar_init(bar + XB_S_FULL, 1);
     mbar_init(bar + XB_DP_FULL, 1);
-    mbar_init(bar + XB_P_FULL, 256);
-    mbar_init(bar + XB_DS_FULL, 256);
+    mbar_init(bar + XB_P_FULL, 8);            // a lane of each warp
+    mbar_init(bar + XB_DS_FULL, 8);
     mbar_init(bar + XB_DV_DONE, 1);
     mbar_init(bar + XB_DK_DONE, 1);
     mbar_init(bar + XB_ACC_FULL, 1);
-    mbar_init(bar + XB_ACC_EMPTY, 256);
+    mbar_init(bar + XB_ACC_EMPTY, 8);
     mbar_init(bar + XB_DRAIN, 1);
+    mbar_init(bar + XB_DRAIN + 1, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -283,16 +288,18 @@ __global__ void __launch_bounds__(kWbThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;          // S, dP, dV, dK or dQ: 128 columns each
   // k-th completion of a barrier has parity k & 1; the whole warp decides together
-  auto W = [&](int id, int64_t k) {
-    return __all_sync(0xffffffffu,
-                      mbar_wait(bar + id, (uint32_t)(k & 1), abort_flag, err));
+  auto W = [&](int id, uint32_t k) {
+    return __all_sync(0xffffffffu, mbar_wait(bar + id, k & 1u, abort_flag, err));
+  };
+  auto arrive = [&](int id) {                // for the whole warp
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar + id);
   };
   // the k-th item's number for a reading warp (-1: no more)
-  auto next_item = [&](int64_t k, int32_t& idx) {
+  auto next_item = [&](uint32_t k, int32_t& idx) {
     if (!W(XB_ITEM_FULL + (int)(k & 1), k >> 1)) return false;
     idx = item_slot[k & 1];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar + XB_ITEM_EMPTY + (int)(k & 1));
+    arrive(XB_ITEM_EMPTY + (int)(k & 1));
     return idx >= 0;
   };
   const int32_t tpt = 128 / a.R;             // tokens per query tile
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
       }
-      int64_t n = 0, ni = 0;                 // streamed tiles, items with tiles
+      uint32_t n = 0, ni = 0;                // streamed tiles, items with tiles
       bool ok = true;
       auto load_rows = [&](uint8_t* dst, uint64_t* b, int32_t tile) {
         for (int h = 0; h < 2; ++h) {
@@ -323,7 +330,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
           tma_load_4d(dst + 32768 + h * 16384, &tm_v, b, h * 64, key0, it.g, it.b);
         }
       };
-      for (int64_t k = 0; ok; ++k) {
+      for (uint32_t k = 0; ok; ++k) {
         if (k >= 2 && !W(XB_ITEM_EMPTY + (int)(k & 1), (k >> 1) - 1)) break;
         int32_t idx = 0;
         if (lane == 0) {
@@ -356,118 +363,145 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       }
       // no copy may still be writing shared memory when the block exits
       if (lane == 0) {
-        for (int64_t k = n > 2 ? n - 2 : 0; k < n; ++k)
+        for (uint32_t k = n > 2 ? n - 2 : 0; k < n; ++k)
           mbar_drain(bar + XB_STR_FULL + (int)(k & 1), (uint32_t)((k >> 1) & 1), err);
         if (ni > 0) mbar_drain(bar + XB_STAY_FULL, (uint32_t)((ni - 1) & 1), err);
       }
     } else if (warp == 9) {
-      // ---------------- MMA ----------------
-      constexpr uint32_t kIdT = idesc_bf16_f32(128, 128, 0), kIdA = idesc_bf16_f32(128, 128, 1);
-      const uint32_t sa = smem_u32(base + kWbOffStay);
-      int64_t n = 0, ni = 0, nv = 0;         // tiles, items with tiles, dV products
+      // ---------------- S, dP ----------------
+      constexpr uint32_t kIdT = idesc_bf16_f32(128, 128, 0);
+      const uint32_t sa = smem_u32(base + kWbOffStay), str = smem_u32(base + kWbOffStream);
+      uint32_t n = 0, ni = 0, nv = 0;        // tiles, items with tiles, dV products before
       int32_t idx;
+      bool ok = true;
       // D = X Y^T of two 128 x 128 tiles in shared memory
-      auto mma_t = [&](uint32_t d, uint32_t xa, uint32_t ya) {
+      auto product = [&](uint32_t d, uint32_t xa, uint32_t ya) {
+        const uint64_t xd = smem_desc_sw128(xa, 16, 1024), yd = smem_desc_sw128(ya, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-          umma_bf16(d, smem_desc_sw128(xa + off, 16, 1024), smem_desc_sw128(ya + off, 16, 1024),
-                    kIdT, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < 8; ++kk) {     // the start address counts 16-byte units
+          const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) / 16;
+          umma_bf16(d, xd + off, yd + off, kIdT, kk > 0 ? 1u : 0u);
         }
-      };
-      // D (+)= X Y, X (bf16, two halves of 64) in TMEM, Y in shared memory
-      auto mma_acc = [&](uint32_t d, uint32_t x, uint32_t ya, bool add) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_bf16_ts(d, x + (kk >> 2) * 64 + (kk & 3) * 8,
-                       smem_desc_sw128(ya + kk * 2048, 16384, 1024), kIdA,
-                       add || kk > 0 ? 1u : 0u);
       };
       // slot of tile t (number m): copies landed, rows past the sequence cleared:
       // they may hold anything, and their P and dS are 0, but 0 * NaN is not
-      auto landed = [&](int32_t t, int64_t m) {
+      auto landed = [&](int32_t t, uint32_t m) {
         const int s = (int)(m & 1);
         if (!W(XB_STR_FULL + s, m >> 1)) return false;
-        uint8_t* tile = base + kWbOffStream + s * 65536;
-        if (it.dkv) {
-          const int64_t r0 =
-              ((int64_t)it.len - a.q_pos0 - (int64_t)(it.q_tile + t) * tpt) * a.R;
-          if (it.len < a.n_kv && r0 < 128) {
-            win_clear_rows(tile, (int32_t)r0, lane);
-            win_clear_rows(tile + 32768, (int32_t)r0, lane);
+        if (it.len < a.n_kv) {
+          uint8_t* tile = base + kWbOffStream + s * 65536;
+          if (it.dkv) {
+            const int32_t r0 = (it.len - (int32_t)a.q_pos0 - (it.q_tile + t) * tpt) * a.R;
+            if (r0 < 128) {
+              win_clear_rows(tile, r0, lane);
+              win_clear_rows(tile + 32768, r0, lane);
+            }
+          } else {
+            const int32_t k0 = win_key0(it.w, t);
+            if (k0 + 128 > it.len) win_clear_rows(tile, it.len - k0, lane);
           }
-        } else {
-          const int32_t k0 = win_key0(it.w, t);
-          if (it.len < a.n_kv && k0 + 128 > it.len) win_clear_rows(tile, it.len - k0, lane);
         }
         return true;
       };
-      auto issue_s = [&](int64_t m) {
+      auto issue_s = [&](uint32_t m) {
         tc_fence_after();
-        if (lane == 0) {
-          mma_t(tmem, sa, smem_u32(base + kWbOffStream + (int)(m & 1) * 65536));
+        if (elect_one()) {
+          product(tmem, sa, str + (m & 1) * 65536);
           umma_commit(bar + XB_S_FULL);
         }
         __syncwarp();
       };
-      bool ok = true;
-      for (int64_t k = 0; ok && next_item(k, idx); ++k) {
+      for (uint32_t k = 0; ok && next_item(k, idx); ++k) {
         wb_item(it, p, idx);
         if (it.nt == 0) continue;
-        ok = W(XB_STAY_FULL, ni) && landed(0, n) && (nv == 0 || W(XB_DV_DONE, nv - 1));
+        const bool dkv = it.dkv;
+        // S overwrites the columns P was read from (dq items keep P in registers)
+        ok = W(XB_STAY_FULL, ni) && landed(0, n) && (nv == 0 || W(XB_DV_DONE, nv - 1)) &&
+             (n == 0 || W(XB_P_FULL, n - 1));
         if (!ok) break;
         issue_s(n);
         for (int32_t t = 0; t < it.nt; ++t, ++n) {
-          const uint32_t str = smem_u32(base + kWbOffStream + (int)(n & 1) * 65536);
           const bool last = t + 1 == it.nt;
           // dP overwrites the columns dS was read from
           if (n > 0 && !W(XB_DK_DONE, n - 1)) { ok = false; break; }
           tc_fence_after();
-          if (lane == 0) {
-            mma_t(tmem + 128, sa + 32768, str + 32768);
+          if (elect_one()) {
+            product(tmem + 128, sa + 32768, str + (n & 1) * 65536 + 32768);
             umma_commit(bar + XB_DP_FULL);
             if (last) umma_commit(bar + XB_STAY_EMPTY);
           }
           __syncwarp();
-          if (!W(XB_P_FULL, n)) { ok = false; break; }
-          if (t == 0 && ni > 0 && !W(XB_ACC_EMPTY, ni - 1)) { ok = false; break; }
-          tc_fence_after();
-          if (it.dkv) {
-            if (lane == 0) {
-              mma_acc(tmem + 256, tmem, str + 32768, t > 0);
-              umma_commit(bar + XB_DV_DONE);
-            }
-            __syncwarp();
-            ++nv;
-          }
-          if (!last) {                        // S overwrites the columns P was read from
-            if (!landed(t + 1, n + 1) || (it.dkv && !W(XB_DV_DONE, nv - 1))) { ok = false; break; }
+          if (dkv) ++nv;
+          if (!last) {
+            if (!landed(t + 1, n + 1)) { ok = false; break; }
+            if (!(dkv ? W(XB_DV_DONE, nv - 1) : W(XB_P_FULL, n))) { ok = false; break; }
             issue_s(n + 1);
           }
-          if (!W(XB_DS_FULL, n)) { ok = false; break; }
-          tc_fence_after();
-          if (lane == 0) {
-            mma_acc(tmem + 384, tmem + 128, str, t > 0);
-            umma_commit(bar + XB_STR_EMPTY + (int)(n & 1));
-            umma_commit(bar + XB_DK_DONE);
-            if (last) umma_commit(bar + XB_ACC_FULL);
-          }
-          __syncwarp();
         }
         ++ni;
       }
       // every MMA issued has finished before the tensor memory is freed
-      if (lane == 0) {
+      if (elect_one()) {
         umma_commit(bar + XB_DRAIN);
         mbar_drain(bar + XB_DRAIN, 0, err);
       }
       __syncwarp();
     } else if (warp == 10) {
-      // ---------------- -lse log2 e and -D of the streamed query rows ----------------
-      int64_t n = 0;
+      // ---------------- dV, dK or dQ ----------------
+      constexpr uint32_t kIdA = idesc_bf16_f32(128, 128, 1);
+      const uint32_t str0 = smem_u32(base + kWbOffStream);
+      uint32_t n = 0, ni = 0;
       int32_t idx;
       bool ok = true;
-      for (int64_t k = 0; ok && next_item(k, idx); ++k) {
+      // D (+)= X Y, X (bf16, two halves of 64) in TMEM, Y in shared memory
+      auto product = [&](uint32_t d, uint32_t x, uint32_t ya, bool add) {
+        const uint64_t yd = smem_desc_sw128(ya, 16384, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_bf16_ts(d, x + (kk >> 2) * 64 + (kk & 3) * 8, yd + kk * (2048 / 16), kIdA,
+                       add || kk > 0 ? 1u : 0u);
+      };
+      for (uint32_t k = 0; ok && next_item(k, idx); ++k) {
+        wb_item(it, p, idx);
+        if (it.nt == 0) continue;
+        const bool dkv = it.dkv;
+        const int32_t nt = it.nt;
+        if (ni > 0 && !W(XB_ACC_EMPTY, ni - 1)) { ok = false; break; }
+        for (int32_t t = 0; t < nt; ++t, ++n) {
+          const uint32_t str = str0 + (n & 1) * 65536;
+          if (!W(XB_STR_FULL + (int)(n & 1), n >> 1)) { ok = false; break; }
+          if (dkv) {
+            if (!W(XB_P_FULL, n)) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+              product(tmem + 256, tmem, str + 32768, t > 0);
+              umma_commit(bar + XB_DV_DONE);
+            }
+            __syncwarp();
+          }
+          if (!W(XB_DS_FULL, n)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            product(tmem + 384, tmem + 128, str, t > 0);
+            umma_commit(bar + XB_STR_EMPTY + (int)(n & 1));
+            umma_commit(bar + XB_DK_DONE);
+            if (t + 1 == nt) umma_commit(bar + XB_ACC_FULL);
+          }
+          __syncwarp();
+        }
+        ++ni;
+      }
+      if (elect_one()) {
+        umma_commit(bar + XB_DRAIN + 1);
+        mbar_drain(bar + XB_DRAIN + 1, 0, err);
+      }
+      __syncwarp();
+    } else {
+      // ---------------- -lse log2 e and -D of the streamed query rows ----------------
+      uint32_t n = 0;
+      int32_t idx;
+      bool ok = true;
+      for (uint32_t k = 0; ok && next_item(k, idx); ++k) {
         wb_item(it, p, idx);
         for (int32_t t = 0; t < it.nt; ++t, ++n) {
           const int s = (int)(n & 1);
@@ -483,9 +517,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
               m[r] = live ? -log2e * __ldg(a.lse + row) : -INFINITY;
               m[128 + r] = live ? -__ldg(p.delta + row) : 0.f;
             }
-            __syncwarp();
           }
-          if (lane == 0) mbar_arrive(bar + XB_META_FULL + s);
+          arrive(XB_META_FULL + s);
         }
       }
     }
@@ -498,10 +531,10 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     const float scale_log2 = a.scale * log2e;
     const uint64_t scale2 = pack_f32x2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
     const int64_t H = (int64_t)a.G * a.R;
-    int64_t n = 0, ni = 0;
+    uint32_t n = 0, ni = 0;
     int32_t idx;
     bool ok = true;
-    for (int64_t k = 0; ok && next_item(k, idx); ++k) {
+    for (uint32_t k = 0; ok && next_item(k, idx); ++k) {
       wb_item(it, p, idx);
       // dq: this thread's query row
       const int32_t i_row = it.dkv ? 0 : it.w.i0 + row / a.R;
@@ -514,69 +547,62 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         nd = -__ldg(p.delta + qrow);
       }
       const int32_t win = a.window > 0 ? (int32_t)min64(a.window, int64_t(1) << 30) : 1 << 30;
-      for (int32_t t = 0; t < it.nt; ++t, ++n) {
-        // visible columns of this thread's 64, as bits
-        uint64_t vis;
-        if (it.dkv) {                         // columns: rows of query tile q_tile + t
-          const int32_t t0 = (int32_t)a.q_pos0 + (it.q_tile + t) * tpt;
-          const int32_t lo = (pos - t0) * a.R;
-          const int32_t d = pos + win - t0;   // first query (of the tile) past the window
-          vis = range_bits(pos - t0 > tpt ? 128 : lo, pos < a.sink || d > tpt ? 128 : d * a.R, c0);
-        } else {                              // columns: keys
-          const int32_t k0 = win_key0(it.w, t);
-          if (t < it.w.ns) {
-            vis = range_bits(0, it.w.s_end - k0, c0);
-          } else {
-            vis = range_bits(max(pos - win + 1 - k0, 0), min(pos - k0 + 1, 128), c0) |
-                  range_bits(0, (int32_t)min64(min64(a.sink - k0, pos - k0 + 1), 128), c0);
-          }
-        }
+      const int32_t sink = (int32_t)a.sink;
+      // one tile; kDkv: lse and D come with the columns, P goes to the tensor core too
+      auto tile = [&](auto kind, uint64_t vis) {
+        constexpr bool kDkv = decltype(kind)::value;
         const bool full = __all_sync(0xffffffffu, vis == ~0ull);
         const float* m = reinterpret_cast<const float*>(base + kWbOffMeta + (int)(n & 1) * 1024) +
                          c0;
-        if (!W(XB_S_FULL, n)) { ok = false; break; }
-        if (!W(XB_META_FULL + (int)(n & 1), n >> 1)) { ok = false; break; }
+        if (!W(XB_META_FULL + (int)(n & 1), n >> 1) || !W(XB_S_FULL, n)) return false;
         tc_fence_after();
         uint32_t s[64];
         tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(s));
         tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
         tmem_ld_wait();
         const uint64_t nl2 = pack_f32x2(__float_as_uint(nl), __float_as_uint(nl));
+        auto weigh = [&](int cc) {            // columns c0 + 32 cc .. + 31
+          uint32_t pk[16];
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {        // columns c0 + 4 q .. + 3
-          uint64_t l0 = nl2, l1 = nl2;
-          if (it.dkv) {
-            const ulonglong2 v = reinterpret_cast<const ulonglong2*>(m)[q];
-            l0 = v.x;
-            l1 = v.y;
+          for (int q = 0; q < 8; ++q) {
+            uint64_t l0 = nl2, l1 = nl2;
+            if (kDkv) {
+              const ulonglong2 v = reinterpret_cast<const ulonglong2*>(m)[8 * cc + q];
+              l0 = v.x;
+              l1 = v.y;
+            }
+            const int c = 32 * cc + 4 * q;
+            float e[4];
+            unpack_f32x2(fma_f32x2(pack_f32x2(s[c], s[c + 1]), scale2, l0), e[0], e[1]);
+            unpack_f32x2(fma_f32x2(pack_f32x2(s[c + 2], s[c + 3]), scale2, l1), e[2], e[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[c + i] = __float_as_uint(ex2_approx(e[i]));
           }
-          float u, v;
-          unpack_f32x2(fma_f32x2(pack_f32x2(s[4 * q], s[4 * q + 1]), scale2, l0), u, v);
-          s[4 * q] = __float_as_uint(ex2_approx(u));
-          s[4 * q + 1] = __float_as_uint(ex2_approx(v));
-          unpack_f32x2(fma_f32x2(pack_f32x2(s[4 * q + 2], s[4 * q + 3]), scale2, l1), u, v);
-          s[4 * q + 2] = __float_as_uint(ex2_approx(u));
-          s[4 * q + 3] = __float_as_uint(ex2_approx(v));
-        }
-        if (!full) {
+          if (!full) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!((vis >> c) & 1)) s[c] = 0u;
-        }
-        if (it.dkv) {
-#pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            uint32_t pk[16];
+            for (int c = 32 * cc; c < 32 * cc + 32; ++c)
+              if (!((vis >> c) & 1)) s[c] = 0u;
+          }
+          if (kDkv) {
 #pragma unroll
             for (int q = 0; q < 16; ++q)
               pk[q] = pack_bf16x2(u2f(s[32 * cc + 2 * q]), u2f(s[32 * cc + 2 * q + 1]));
             tmem_st_32x32b_x16(ts + 16 * cc, pk);
           }
+        };
+        if (kDkv) {
+          weigh(0);
+          weigh(1);
           tmem_st_wait();
+          tc_fence_before();
+          arrive(XB_P_FULL);
+        } else {                              // S is in registers: the next one may come
+          tc_fence_before();
+          arrive(XB_P_FULL);
+          weigh(0);
+          weigh(1);
         }
-        tc_fence_before();
-        mbar_arrive(bar + XB_P_FULL);
-        if (!W(XB_DP_FULL, n)) { ok = false; break; }
+        if (!W(XB_DP_FULL, n)) return false;
         tc_fence_after();
         const uint64_t nd2 = pack_f32x2(__float_as_uint(nd), __float_as_uint(nd));
         uint32_t pk[32];
@@ -588,34 +614,53 @@ __global__ void __launch_bounds__(kWbThreads, 1)
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             uint64_t d0 = nd2, d1 = nd2;
-            if (it.dkv) {
+            if (kDkv) {
               const ulonglong2 v = reinterpret_cast<const ulonglong2*>(m + 128)[8 * cc + q];
               d0 = v.x;
               d1 = v.y;
             }
             const int c = 32 * cc + 4 * q;
-            float u, v;
+            float e[4];
             unpack_f32x2(mul_f32x2(pack_f32x2(s[c], s[c + 1]),
-                                   add_f32x2(pack_f32x2(d[4 * q], d[4 * q + 1]), d0)), u, v);
-            if (!full) {                      // dO.v may be anything where nothing is seen
-              u = (vis >> c) & 1 ? u : 0.f;
-              v = (vis >> (c + 1)) & 1 ? v : 0.f;
-            }
-            pk[16 * cc + 2 * q] = pack_bf16x2(u, v);
+                                   add_f32x2(pack_f32x2(d[4 * q], d[4 * q + 1]), d0)), e[0], e[1]);
             unpack_f32x2(mul_f32x2(pack_f32x2(s[c + 2], s[c + 3]),
-                                   add_f32x2(pack_f32x2(d[4 * q + 2], d[4 * q + 3]), d1)), u, v);
-            if (!full) {
-              u = (vis >> (c + 2)) & 1 ? u : 0.f;
-              v = (vis >> (c + 3)) & 1 ? v : 0.f;
+                                   add_f32x2(pack_f32x2(d[4 * q + 2], d[4 * q + 3]), d1)), e[2],
+                         e[3]);
+            if (!full) {                      // dO.v may be anything where nothing is seen
+#pragma unroll
+              for (int i = 0; i < 4; ++i) e[i] = (vis >> (c + i)) & 1 ? e[i] : 0.f;
             }
-            pk[16 * cc + 2 * q + 1] = pack_bf16x2(u, v);
+            pk[16 * cc + 2 * q] = pack_bf16x2(e[0], e[1]);
+            pk[16 * cc + 2 * q + 1] = pack_bf16x2(e[2], e[3]);
           }
         }
         tmem_st_32x32b_x16(ts + 128, *reinterpret_cast<uint32_t(*)[16]>(pk));
         tmem_st_32x32b_x16(ts + 144, *reinterpret_cast<uint32_t(*)[16]>(pk + 16));
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar + XB_DS_FULL);
+        arrive(XB_DS_FULL);
+        ++n;
+        return true;
+      };
+      // visible columns of this thread's 64, as bits
+      if (it.dkv) {                           // columns: rows of query tile q_tile + t
+        const bool sees_all = pos < sink;
+        int32_t d = pos - (int32_t)a.q_pos0 - it.q_tile * tpt;   // first query that sees the key
+        for (int32_t t = 0; ok && t < it.nt; ++t, d -= tpt) {
+          const int32_t e = d + win;                             // first one past the window
+          ok = tile(std::true_type{},
+                    range_bits(d > tpt ? 128 : d * a.R, sees_all || e > tpt ? 128 : e * a.R, c0));
+        }
+      } else {                                // columns: keys
+        for (int32_t t = 0; ok && t < it.nt; ++t) {
+          const int32_t k0 = win_key0(it.w, t);
+          const uint64_t vis =
+              t < it.w.ns
+                  ? range_bits(0, it.w.s_end - k0, c0)
+                  : range_bits(max(pos - win + 1 - k0, 0), min(pos - k0 + 1, 128), c0) |
+                        range_bits(0, min(min(sink - k0, pos - k0 + 1), 128), c0);
+          ok = tile(std::false_type{}, vis);
+        }
       }
       if (!ok) break;
       // outputs: dk, dv items: warps 0-3 dV, 4-7 dK, a row of 128 each; dq: 64 columns each
@@ -666,7 +711,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       }
       if (any) {
         tc_fence_before();
-        mbar_arrive(bar + XB_ACC_EMPTY);
+        arrive(XB_ACC_EMPTY);
         ++ni;
       }
     }
