@@ -23,9 +23,13 @@
 //   warp 9          issues S and dP;  warp 10  issues dV and dK or dQ (the issue of
 //                   eight MMAs takes as long as they do: one warp for all of them
 //                   left the tensor core waiting)
-// TMEM: S (P in place, bf16), dP (dS in place), dV, dK or dQ: 128 columns each.
-// Per tile the tensor core runs dP(n), dV(n), S(n+1), dK(n): the exponentials of
-// n+1 run under dK(n) and dP(n+1), the dS of n under dV(n) and S(n+1).
+// TMEM: two tile buffers, dV, dK or dQ: 128 columns each.  A tile lives in one
+// buffer: S(n), read into registers; dP(n) over it, made while the exponentials are
+// at work; then P(n) and dS(n) (bf16) over that, the A operands of the sums.  Tiles
+// alternate between the buffers, so the sums of n - 1 and S(n + 1) run beside the
+// softmax of n.  (With one buffer for S and P, another for dP and dS, S(n + 1) had to
+// wait for dV(n): 4300 clocks a tile.)  Per tile: dP(n), dK(n-1), dV(n-1), S(n+1);
+// Q and dO slots are freed apart, Q first, since S(n + 2) needs only that.
 // A key block that many queries see (sinks; no window) is cut into chunks of
 // query tiles whose fp32 sums a last kernel adds in chunk order.
 #include <type_traits>
@@ -38,7 +42,7 @@ namespace msa {
 
 namespace {
 constexpr int kWbThreads = 384;
-constexpr int kWbRegsAtLaunch = 168, kWbRegsControl = 88, kWbRegsMath = 208;
+constexpr int kWbRegsAtLaunch = 168, kWbRegsControl = 72, kWbRegsMath = 216;
 static_assert(kWbRegsControl + 2 * kWbRegsMath == 3 * kWbRegsAtLaunch,
               "warpgroup register shares must add up to the launch allocation");
 constexpr int kWbOffStay = 0;                          // K, V or Q, dO: 32 KB each
@@ -47,8 +51,8 @@ constexpr int kWbOffMeta = kWbOffStream + 2 * 65536;   // two slots: -lse log2 e
 constexpr int kWbOffBar = kWbOffMeta + 2 * 1024;
 enum {
   XB_ITEM_FULL = 0, XB_ITEM_EMPTY = 2, XB_STAY_FULL = 4, XB_STAY_EMPTY, XB_STR_FULL = 6,
-  XB_STR_EMPTY = 8, XB_META_FULL = 10, XB_S_FULL = 12, XB_DP_FULL, XB_P_FULL, XB_DS_FULL, XB_DV_DONE, XB_DK_DONE,
-  XB_ACC_FULL, XB_ACC_EMPTY, XB_DRAIN, XB_COUNT = XB_DRAIN + 2
+  XB_STR_EMPTY = 10, XB_META_FULL = 14, XB_DS_FULL = 16, XB_DONE = 18, XB_S_FULL = 20, XB_S_READ,
+  XB_DP_FULL, XB_ACC_FULL, XB_ACC_EMPTY, XB_DRAIN, XB_COUNT = XB_DRAIN + 2
 };
 constexpr int kWbOffMisc = kWbOffBar + XB_COUNT * 8;
 constexpr int kWbSmemBytes = 1024 + kWbOffMisc + 32;
@@ -260,18 +264,19 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar + XB_ITEM_FULL + s, 1);
       mbar_init(bar + XB_ITEM_EMPTY + s, kWbItemReaders);
-      mbar_init(bar + XB_STR_FULL + s, 1);
-      mbar_init(bar + XB_STR_EMPTY + s, 1);
+      for (int h = 0; h < 2; ++h) {                 // slot s: Q or K at 2 s, dO or V at 2 s + 1
+        mbar_init(bar + XB_STR_FULL + 2 * s + h, 1);
+        mbar_init(bar + XB_STR_EMPTY + 2 * s + h, 1);
+      }
       mbar_init(bar + XB_META_FULL + s, 1);
+      mbar_init(bar + XB_DS_FULL + s, 8);           // a lane of each warp
+      mbar_init(bar + XB_DONE + s, 1);
     }
     mbar_init(bar + XB_STAY_FULL, 1);
     mbar_init(bar + XB_STAY_EMPTY, 1);
     mbar_init(bar + XB_S_FULL, 1);
+    mbar_init(bar + XB_S_READ, 8);
     mbar_init(bar + XB_DP_FULL, 1);
-    mbar_init(bar + XB_P_FULL, 8);            // a lane of each warp
-    mbar_init(bar + XB_DS_FULL, 8);
-    mbar_init(bar + XB_DV_DONE, 1);
-    mbar_init(bar + XB_DK_DONE, 1);
     mbar_init(bar + XB_ACC_FULL, 1);
     mbar_init(bar + XB_ACC_EMPTY, 8);
     mbar_init(bar + XB_DRAIN, 1);
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;          // S, dP, dV, dK or dQ: 128 columns each
+  const uint32_t tmem = *tmem_slot;          // tile buffers 0, 1, dV, dK or dQ: 128 columns each
   // k-th completion of a barrier has parity k & 1; the whole warp decides together
   auto W = [&](int id, uint32_t k) {
     return __all_sync(0xffffffffu, mbar_wait(bar + id, k & 1u, abort_flag, err));
@@ -316,19 +321,11 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
       }
-      uint32_t n = 0, ni = 0;                // streamed tiles, items with tiles
+      uint32_t n = 0, ni = 0, issued[2] = {0, 0};   // streamed tiles, items with tiles
       bool ok = true;
-      auto load_rows = [&](uint8_t* dst, uint64_t* b, int32_t tile) {
-        for (int h = 0; h < 2; ++h) {
-          tma_load_4d(dst + h * 16384, &tm_q, b, h * 64, it.g * a.R, tile * tpt, it.b);
-          tma_load_4d(dst + 32768 + h * 16384, &tm_do, b, h * 64, it.g * a.R, tile * tpt, it.b);
-        }
-      };
-      auto load_keys = [&](uint8_t* dst, uint64_t* b, int32_t key0) {
-        for (int h = 0; h < 2; ++h) {
-          tma_load_4d(dst + h * 16384, &tm_k, b, h * 64, key0, it.g, it.b);
-          tma_load_4d(dst + 32768 + h * 16384, &tm_v, b, h * 64, key0, it.g, it.b);
-        }
+      auto load = [&](uint8_t* dst, const CUtensorMap* tm, uint64_t* b, int32_t y, int32_t z) {
+        tma_load_4d(dst, tm, b, 0, y, z, it.b);
+        tma_load_4d(dst + 16384, tm, b, 64, y, z, it.b);
       };
       for (uint32_t k = 0; ok; ++k) {
         if (k >= 2 && !W(XB_ITEM_EMPTY + (int)(k & 1), (k >> 1) - 1)) break;
@@ -346,32 +343,40 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         if (ni > 0 && !W(XB_STAY_EMPTY, ni - 1)) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar + XB_STAY_FULL, 65536u);
-          if (it.dkv) load_keys(base + kWbOffStay, bar + XB_STAY_FULL, it.k0);
-          else load_rows(base + kWbOffStay, bar + XB_STAY_FULL, it.w.i0 / tpt);
+          const int32_t y = it.dkv ? it.k0 : it.g * a.R, z = it.dkv ? it.g : it.w.i0;
+          load(base + kWbOffStay, it.dkv ? &tm_k : &tm_q, bar + XB_STAY_FULL, y, z);
+          load(base + kWbOffStay + 32768, it.dkv ? &tm_v : &tm_do, bar + XB_STAY_FULL, y, z);
         }
         ++ni;
         for (int32_t t = 0; t < it.nt; ++t, ++n) {
-          const int s = (int)(n & 1);
-          if (n >= 2 && !W(XB_STR_EMPTY + s, (n >> 1) - 1)) { ok = false; break; }
-          if (lane == 0) {
-            uint8_t* dst = base + kWbOffStream + s * 65536;
-            mbar_arrive_expect_tx(bar + XB_STR_FULL + s, 65536u);
-            if (it.dkv) load_rows(dst, bar + XB_STR_FULL + s, it.q_tile + t);
-            else load_keys(dst, bar + XB_STR_FULL + s, win_key0(it.w, t));
+          const int32_t y = it.dkv ? it.g * a.R : win_key0(it.w, t);
+          const int32_t z = it.dkv ? (it.q_tile + t) * tpt : it.g;
+          for (int h = 0; ok && h < 2; ++h) {
+            const int s = 2 * (int)(n & 1) + h;
+            ok = n < 2 || W(XB_STR_EMPTY + s, (n >> 1) - 1);
+            if (ok && lane == 0) {
+              mbar_arrive_expect_tx(bar + XB_STR_FULL + s, 32768u);
+              load(base + kWbOffStream + s * 32768,
+                   it.dkv ? (h ? &tm_do : &tm_q) : (h ? &tm_v : &tm_k), bar + XB_STR_FULL + s, y,
+                   z);
+            }
+            if (ok) issued[h] = n + 1;
           }
+          if (!ok) break;
         }
       }
       // no copy may still be writing shared memory when the block exits
       if (lane == 0) {
-        for (uint32_t k = n > 2 ? n - 2 : 0; k < n; ++k)
-          mbar_drain(bar + XB_STR_FULL + (int)(k & 1), (uint32_t)((k >> 1) & 1), err);
+        for (int h = 0; h < 2; ++h)
+          for (uint32_t k = issued[h] > 2 ? issued[h] - 2 : 0; k < issued[h]; ++k)
+            mbar_drain(bar + XB_STR_FULL + 2 * (int)(k & 1) + h, (k >> 1) & 1u, err);
         if (ni > 0) mbar_drain(bar + XB_STAY_FULL, (uint32_t)((ni - 1) & 1), err);
       }
     } else if (warp == 9) {
       // ---------------- S, dP ----------------
       constexpr uint32_t kIdT = idesc_bf16_f32(128, 128, 0);
       const uint32_t sa = smem_u32(base + kWbOffStay), str = smem_u32(base + kWbOffStream);
-      uint32_t n = 0, ni = 0, nv = 0;        // tiles, items with tiles, dV products before
+      uint32_t n = 0, ni = 0;                // tiles, items with tiles
       int32_t idx;
       bool ok = true;
       // D = X Y^T of two 128 x 128 tiles in shared memory
@@ -383,60 +388,52 @@ __global__ void __launch_bounds__(kWbThreads, 1)
           umma_bf16(d, xd + off, yd + off, kIdT, kk > 0 ? 1u : 0u);
         }
       };
-      // slot of tile t (number m): copies landed, rows past the sequence cleared:
-      // they may hold anything, and their P and dS are 0, but 0 * NaN is not
-      auto landed = [&](int32_t t, uint32_t m) {
-        const int s = (int)(m & 1);
+      // half h (Q or K; dO or V) of tile t (number m) has landed; its rows past the
+      // sequence are cleared: they may hold anything, and their P and dS are 0, but
+      // 0 * NaN is not.  (V needs none: a column of dP that nobody sees is dropped.)
+      auto landed = [&](int h, int32_t t, uint32_t m) {
+        const int s = 2 * (int)(m & 1) + h;
         if (!W(XB_STR_FULL + s, m >> 1)) return false;
-        if (it.len < a.n_kv) {
-          uint8_t* tile = base + kWbOffStream + s * 65536;
-          if (it.dkv) {
-            const int32_t r0 = (it.len - (int32_t)a.q_pos0 - (it.q_tile + t) * tpt) * a.R;
-            if (r0 < 128) {
-              win_clear_rows(tile, r0, lane);
-              win_clear_rows(tile + 32768, r0, lane);
-            }
-          } else {
-            const int32_t k0 = win_key0(it.w, t);
-            if (k0 + 128 > it.len) win_clear_rows(tile, it.len - k0, lane);
-          }
+        if (it.len < a.n_kv && (it.dkv || h == 0)) {
+          const int32_t r0 = it.dkv
+                                 ? (it.len - (int32_t)a.q_pos0 - (it.q_tile + t) * tpt) * a.R
+                                 : it.len - win_key0(it.w, t);
+          if (r0 < 128) win_clear_rows(base + kWbOffStream + s * 32768, r0, lane);
         }
         return true;
       };
-      auto issue_s = [&](uint32_t m) {
+      // S of tile t, into the buffer that tile m - 2 has left
+      auto issue_s = [&](int32_t t, uint32_t m) {
+        if (!landed(0, t, m)) return false;
+        if (m >= 2 && !W(XB_DONE + (int)(m & 1), (m >> 1) - 1)) return false;
         tc_fence_after();
         if (elect_one()) {
-          product(tmem, sa, str + (m & 1) * 65536);
+          product(tmem + 128 * (m & 1), sa, str + (m & 1) * 65536);
           umma_commit(bar + XB_S_FULL);
         }
         __syncwarp();
+        return true;
       };
       for (uint32_t k = 0; ok && next_item(k, idx); ++k) {
         wb_item(it, p, idx);
         if (it.nt == 0) continue;
         const bool dkv = it.dkv;
-        // S overwrites the columns P was read from (dq items keep P in registers)
-        ok = W(XB_STAY_FULL, ni) && landed(0, n) && (nv == 0 || W(XB_DV_DONE, nv - 1)) &&
-             (n == 0 || W(XB_P_FULL, n - 1));
+        const int32_t nt = it.nt;
+        ok = W(XB_STAY_FULL, ni) && issue_s(0, n);
         if (!ok) break;
-        issue_s(n);
-        for (int32_t t = 0; t < it.nt; ++t, ++n) {
-          const bool last = t + 1 == it.nt;
-          // dP overwrites the columns dS was read from
-          if (n > 0 && !W(XB_DK_DONE, n - 1)) { ok = false; break; }
+        for (int32_t t = 0; t < nt; ++t, ++n) {
+          // dP over S, once that is in registers
+          if (!landed(1, t, n) || !W(XB_S_READ, n)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
-            product(tmem + 128, sa + 32768, str + (n & 1) * 65536 + 32768);
+            const uint32_t b = n & 1;
+            product(tmem + 128 * b, sa + 32768, str + b * 65536 + 32768);
             umma_commit(bar + XB_DP_FULL);
-            if (last) umma_commit(bar + XB_STAY_EMPTY);
+            if (!dkv) umma_commit(bar + XB_STR_EMPTY + 2 * b + 1);      // V's last use
+            if (t + 1 == nt) umma_commit(bar + XB_STAY_EMPTY);
           }
           __syncwarp();
-          if (dkv) ++nv;
-          if (!last) {
-            if (!landed(t + 1, n + 1)) { ok = false; break; }
-            if (!(dkv ? W(XB_DV_DONE, nv - 1) : W(XB_P_FULL, n))) { ok = false; break; }
-            issue_s(n + 1);
-          }
+          if (t + 1 < nt && !issue_s(t + 1, n + 1)) { ok = false; break; }
         }
         ++ni;
       }
@@ -468,23 +465,20 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         const int32_t nt = it.nt;
         if (ni > 0 && !W(XB_ACC_EMPTY, ni - 1)) { ok = false; break; }
         for (int32_t t = 0; t < nt; ++t, ++n) {
-          const uint32_t str = str0 + (n & 1) * 65536;
-          if (!W(XB_STR_FULL + (int)(n & 1), n >> 1)) { ok = false; break; }
-          if (dkv) {
-            if (!W(XB_P_FULL, n)) { ok = false; break; }
-            tc_fence_after();
-            if (elect_one()) {
-              product(tmem + 256, tmem, str + 32768, t > 0);
-              umma_commit(bar + XB_DV_DONE);
-            }
-            __syncwarp();
-          }
-          if (!W(XB_DS_FULL, n)) { ok = false; break; }
+          const uint32_t b = n & 1, str = str0 + b * 65536, x = tmem + 128 * b;
+          // the tiles it reads (landed long ago; V's slot may have been refilled)
+          if (!W(XB_STR_FULL + 2 * (int)b, n >> 1)) { ok = false; break; }
+          if (dkv && !W(XB_STR_FULL + 2 * (int)b + 1, n >> 1)) { ok = false; break; }
+          if (!W(XB_DS_FULL + (int)b, n >> 1)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
-            product(tmem + 384, tmem + 128, str, t > 0);
-            umma_commit(bar + XB_STR_EMPTY + (int)(n & 1));
-            umma_commit(bar + XB_DK_DONE);
+            product(tmem + 384, x + 32, str, t > 0);
+            umma_commit(bar + XB_STR_EMPTY + 2 * b);
+            if (dkv) {
+              product(tmem + 256, x, str + 32768, t > 0);
+              umma_commit(bar + XB_STR_EMPTY + 2 * b + 1);
+            }
+            umma_commit(bar + XB_DONE + b);
             if (t + 1 == nt) umma_commit(bar + XB_ACC_FULL);
           }
           __syncwarp();
@@ -505,7 +499,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         wb_item(it, p, idx);
         for (int32_t t = 0; t < it.nt; ++t, ++n) {
           const int s = (int)(n & 1);
-          if (n >= 2 && !W(XB_STR_EMPTY + s, (n >> 1) - 1)) { ok = false; break; }
+          if (n >= 2 && !W(XB_STR_EMPTY + 2 * s, (n >> 1) - 1)) { ok = false; break; }
           if (it.dkv) {
             float* m = reinterpret_cast<float*>(base + kWbOffMeta + s * 1024);
             for (int r = lane; r < 128; r += 32) {
@@ -527,7 +521,6 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     // ---------------- P, dS; outputs ----------------
     const int half = warp >> 2, row = (warp & 3) * 32 + lane, c0 = 64 * half;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lane_base + c0;
     const float scale_log2 = a.scale * log2e;
     const uint64_t scale2 = pack_f32x2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
     const int64_t H = (int64_t)a.G * a.R;
@@ -548,69 +541,62 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       }
       const int32_t win = a.window > 0 ? (int32_t)min64(a.window, int64_t(1) << 30) : 1 << 30;
       const int32_t sink = (int32_t)a.sink;
-      // one tile; kDkv: lse and D come with the columns, P goes to the tensor core too
+      // one tile; kDkv: lse and D come with the columns, P goes to the tensor core too.
+      // Of its 64 columns of the buffer, P takes the first 32, dS the others
       auto tile = [&](auto kind, uint64_t vis) {
         constexpr bool kDkv = decltype(kind)::value;
         const bool full = __all_sync(0xffffffffu, vis == ~0ull);
         const float* m = reinterpret_cast<const float*>(base + kWbOffMeta + (int)(n & 1) * 1024) +
                          c0;
+        const uint32_t ts = tmem + lane_base + 128 * (n & 1) + c0;
         if (!W(XB_META_FULL + (int)(n & 1), n >> 1) || !W(XB_S_FULL, n)) return false;
         tc_fence_after();
-        uint32_t s[64];
+        uint32_t s[64], d[64];
         tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(s));
         tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
         tmem_ld_wait();
+        tc_fence_before();
+        arrive(XB_S_READ);
         const uint64_t nl2 = pack_f32x2(__float_as_uint(nl), __float_as_uint(nl));
-        auto weigh = [&](int cc) {            // columns c0 + 32 cc .. + 31
-          uint32_t pk[16];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            uint64_t l0 = nl2, l1 = nl2;
-            if (kDkv) {
-              const ulonglong2 v = reinterpret_cast<const ulonglong2*>(m)[8 * cc + q];
-              l0 = v.x;
-              l1 = v.y;
-            }
-            const int c = 32 * cc + 4 * q;
-            float e[4];
-            unpack_f32x2(fma_f32x2(pack_f32x2(s[c], s[c + 1]), scale2, l0), e[0], e[1]);
-            unpack_f32x2(fma_f32x2(pack_f32x2(s[c + 2], s[c + 3]), scale2, l1), e[2], e[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[c + i] = __float_as_uint(ex2_approx(e[i]));
-          }
-          if (!full) {
-#pragma unroll
-            for (int c = 32 * cc; c < 32 * cc + 32; ++c)
-              if (!((vis >> c) & 1)) s[c] = 0u;
-          }
+        for (int q = 0; q < 16; ++q) {        // columns c0 + 4 q .. + 3
+          uint64_t l0 = nl2, l1 = nl2;
           if (kDkv) {
+            const ulonglong2 v = reinterpret_cast<const ulonglong2*>(m)[q];
+            l0 = v.x;
+            l1 = v.y;
+          }
+          const int c = 4 * q;
+          float e[4];
+          unpack_f32x2(fma_f32x2(pack_f32x2(s[c], s[c + 1]), scale2, l0), e[0], e[1]);
+          unpack_f32x2(fma_f32x2(pack_f32x2(s[c + 2], s[c + 3]), scale2, l1), e[2], e[3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[c + i] = __float_as_uint(ex2_approx(e[i]));
+        }
+        if (!full) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!((vis >> c) & 1)) s[c] = 0u;
+        }
+        if (!W(XB_DP_FULL, n)) return false;
+        tc_fence_after();
+        tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(d));
+        tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(d + 32));
+        const uint64_t nd2 = pack_f32x2(__float_as_uint(nd), __float_as_uint(nd));
+        tmem_ld_wait();
+        if (kDkv) {
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t pk[16];
 #pragma unroll
             for (int q = 0; q < 16; ++q)
               pk[q] = pack_bf16x2(u2f(s[32 * cc + 2 * q]), u2f(s[32 * cc + 2 * q + 1]));
             tmem_st_32x32b_x16(ts + 16 * cc, pk);
           }
-        };
-        if (kDkv) {
-          weigh(0);
-          weigh(1);
-          tmem_st_wait();
-          tc_fence_before();
-          arrive(XB_P_FULL);
-        } else {                              // S is in registers: the next one may come
-          tc_fence_before();
-          arrive(XB_P_FULL);
-          weigh(0);
-          weigh(1);
         }
-        if (!W(XB_DP_FULL, n)) return false;
-        tc_fence_after();
-        const uint64_t nd2 = pack_f32x2(__float_as_uint(nd), __float_as_uint(nd));
-        uint32_t pk[32];
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
-          uint32_t d[32];
-          tmem_ld_32x32b_x32(ts + 128 + 32 * cc, d);
-          tmem_ld_wait();
+          uint32_t pk[16];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             uint64_t d0 = nd2, d1 = nd2;
@@ -622,23 +608,21 @@ __global__ void __launch_bounds__(kWbThreads, 1)
             const int c = 32 * cc + 4 * q;
             float e[4];
             unpack_f32x2(mul_f32x2(pack_f32x2(s[c], s[c + 1]),
-                                   add_f32x2(pack_f32x2(d[4 * q], d[4 * q + 1]), d0)), e[0], e[1]);
+                                   add_f32x2(pack_f32x2(d[c], d[c + 1]), d0)), e[0], e[1]);
             unpack_f32x2(mul_f32x2(pack_f32x2(s[c + 2], s[c + 3]),
-                                   add_f32x2(pack_f32x2(d[4 * q + 2], d[4 * q + 3]), d1)), e[2],
-                         e[3]);
+                                   add_f32x2(pack_f32x2(d[c + 2], d[c + 3]), d1)), e[2], e[3]);
             if (!full) {                      // dO.v may be anything where nothing is seen
 #pragma unroll
               for (int i = 0; i < 4; ++i) e[i] = (vis >> (c + i)) & 1 ? e[i] : 0.f;
             }
-            pk[16 * cc + 2 * q] = pack_bf16x2(e[0], e[1]);
-            pk[16 * cc + 2 * q + 1] = pack_bf16x2(e[2], e[3]);
+            pk[2 * q] = pack_bf16x2(e[0], e[1]);
+            pk[2 * q + 1] = pack_bf16x2(e[2], e[3]);
           }
+          tmem_st_32x32b_x16(ts + 32 + 16 * cc, pk);
         }
-        tmem_st_32x32b_x16(ts + 128, *reinterpret_cast<uint32_t(*)[16]>(pk));
-        tmem_st_32x32b_x16(ts + 144, *reinterpret_cast<uint32_t(*)[16]>(pk + 16));
         tmem_st_wait();
         tc_fence_before();
-        arrive(XB_DS_FULL);
+        arrive(XB_DS_FULL + (int)(n & 1));
         ++n;
         return true;
       };
