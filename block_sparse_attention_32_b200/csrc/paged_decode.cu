@@ -125,8 +125,8 @@ __global__ void __launch_bounds__(kPdThreads, 1)
                         const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ PagedDecodeArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  // (an offset, so that the compiler still knows the address space)
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   int32_t* lens = reinterpret_cast<int32_t*>(base + kPdOffLens);
   int32_t* prefix = lens + a.batch;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(kWaThreads, 1)
                            const __grid_constant__ WindowArgs a, int32_t tiles_per_item,
                            int32_t n_items) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  // (an offset, so that the compiler still knows the address space)
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bar = reinterpret_cast<uint64_t*>(base + kWaOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + kWaOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + kWaOffMisc + 4);

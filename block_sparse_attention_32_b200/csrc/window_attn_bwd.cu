@@ -18,11 +18,13 @@
 // both kinds of item through the same roles, dealt by a counter: the short dq
 // items fill the tail that the long dk, dv items leave.  Which CTA takes an item
 // changes no result.
-//   warps 0-3, 4-7  P and dS: thread = accumulator row, columns 0-63 / 64-127
-//   warp 8          scheduler and TMA;  warp 11  -lse, -D of the streamed rows
-//   warp 9          issues S and dP;  warp 10  issues dV and dK or dQ (the issue of
-//                   eight MMAs takes as long as they do: one warp for all of them
-//                   left the tensor core waiting)
+//   warps 0-15  P and dS, four warpgroups: thread = accumulator row x 32 columns (with
+//               two warpgroups a tile's softmax took 3300 clocks, more than its
+//               products: two warps a scheduler do not cover their latencies)
+//   warp 16     scheduler and TMA;  warp 19  -lse, -D of the streamed rows
+//   warp 17     issues S and dP;  warp 18  issues dV and dK or dQ (the issue of eight
+//               MMAs takes as long as they do: one warp for all of them left the
+//               tensor core waiting)
 // TMEM: two tile buffers, dV, dK or dQ: 128 columns each.  A tile lives in one
 // buffer: S(n), read into registers; dP(n) over it, made while the exponentials are
 // at work; then P(n) and dS(n) (bf16) over that, the A operands of the sums.  Tiles
@@ -41,9 +43,12 @@
 namespace msa {
 
 namespace {
-constexpr int kWbThreads = 384;
-constexpr int kWbRegsAtLaunch = 168, kWbRegsControl = 72, kWbRegsMath = 216;
-static_assert(kWbRegsControl + 2 * kWbRegsMath == 3 * kWbRegsAtLaunch,
+constexpr int kWbThreads = 640;
+constexpr int kWbCtl = 16;             // first control warp
+// registers per thread: 96 at launch (65536 / 640 rounded down to the allocation
+// unit; the launcher checks the compiled count)
+constexpr int kWbRegsAtLaunch = 96, kWbRegsControl = 64, kWbRegsMath = 104;
+static_assert(kWbRegsControl + 4 * kWbRegsMath == 5 * kWbRegsAtLaunch,
               "warpgroup register shares must add up to the launch allocation");
 constexpr int kWbOffStay = 0;                          // K, V or Q, dO: 32 KB each
 constexpr int kWbOffStream = 65536;                    // two slots of 64 KB
@@ -55,9 +60,11 @@ enum {
   XB_DP_FULL, XB_ACC_FULL, XB_ACC_EMPTY, XB_DRAIN, XB_COUNT = XB_DRAIN + 2
 };
 constexpr int kWbOffMisc = kWbOffBar + XB_COUNT * 8;
-constexpr int kWbSmemBytes = 1024 + kWbOffMisc + 32;
+constexpr int kWbOffItem = (kWbOffMisc + 16 + 15) / 16 * 16;    // two slots
+constexpr int kWbItemBytes = 160;
+constexpr int kWbSmemBytes = 1024 + kWbOffItem + 2 * kWbItemBytes;
 static_assert(kWbSmemBytes <= 232448, "shared memory per block");
-constexpr int kWbItemReaders = 11;     // warps that read an item's number: 0-7, 9-11
+constexpr int kWbItemReaders = 19;     // warps that read an item's number: all but the scheduler
 constexpr int kWbMinChunk = 32;        // query tiles of a chunk at least
 constexpr int kWbSplit = 2 * 148;      // chunks aimed at when blocks are cut
 
@@ -118,14 +125,16 @@ WbPlan wb_plan(const WindowArgs& a) {
 }
 size_t pad32(size_t n) { return (n + 31) / 32 * 32; }
 
-// one work item, as every role sees it
+// one work item, as every role sees it: decoded once by the scheduler and kept in
+// shared memory, so that the softmax warps need not hold it in registers
 struct WbItem {
-  bool dkv;
+  bool dkv, end;             // end: there are no more
   int32_t b, g, nt;          // nt: streamed tiles
   int32_t k0, q_tile, part;  // dkv: first key, first query tile, partial (-1: final)
   int32_t len;
   WinItem w;                 // dq
 };
+static_assert(sizeof(WbItem) <= kWbItemBytes, "an item's slot");
 __device__ __forceinline__ void wb_item(WbItem& it, const WindowBwdArgs& p, int32_t idx) {
   const WindowArgs& a = p.w;
   const int32_t bg_all = (int32_t)a.batch * a.G;
@@ -157,12 +166,12 @@ __device__ __forceinline__ void wb_item(WbItem& it, const WindowBwdArgs& p, int3
   }
 }
 
-// columns lo .. hi - 1 of the 64 from c0 on, as bits
-__device__ __forceinline__ uint64_t range_bits(int32_t lo, int32_t hi, int32_t c0) {
+// columns lo .. hi - 1 of the 32 from c0 on, as bits
+__device__ __forceinline__ uint32_t range_bits(int32_t lo, int32_t hi, int32_t c0) {
   lo = max(lo - c0, 0);
-  hi = min(hi - c0, 64);
-  if (lo >= hi) return 0ull;
-  return (hi >= 64 ? ~0ull : (1ull << hi) - 1) & ~((1ull << lo) - 1);
+  hi = min(hi - c0, 32);
+  if (lo >= hi) return 0u;
+  return (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
 }
 }  // namespace
 
@@ -250,12 +259,11 @@ __global__ void __launch_bounds__(kWbThreads, 1)
                            const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ WindowBwdArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  // (an offset, so that the compiler still knows the address space)
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bar = reinterpret_cast<uint64_t*>(base + kWbOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + kWbOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + kWbOffMisc + 4);
-  volatile int32_t* item_slot = reinterpret_cast<volatile int32_t*>(base + kWbOffMisc + 8);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const WindowArgs& a = p.w;
   int32_t* err = a.err;
@@ -269,22 +277,22 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         mbar_init(bar + XB_STR_EMPTY + 2 * s + h, 1);
       }
       mbar_init(bar + XB_META_FULL + s, 1);
-      mbar_init(bar + XB_DS_FULL + s, 8);           // a lane of each warp
+      mbar_init(bar + XB_DS_FULL + s, 16);          // a lane of each warp
       mbar_init(bar + XB_DONE + s, 1);
     }
     mbar_init(bar + XB_STAY_FULL, 1);
     mbar_init(bar + XB_STAY_EMPTY, 1);
     mbar_init(bar + XB_S_FULL, 1);
-    mbar_init(bar + XB_S_READ, 8);
+    mbar_init(bar + XB_S_READ, 16);
     mbar_init(bar + XB_DP_FULL, 1);
     mbar_init(bar + XB_ACC_FULL, 1);
-    mbar_init(bar + XB_ACC_EMPTY, 8);
+    mbar_init(bar + XB_ACC_EMPTY, 16);
     mbar_init(bar + XB_DRAIN, 1);
     mbar_init(bar + XB_DRAIN + 1, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == 9) {
+  if (warp == kWbCtl + 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -300,20 +308,20 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(bar + id);
   };
-  // the k-th item's number for a reading warp (-1: no more)
-  auto next_item = [&](uint32_t k, int32_t& idx) {
-    if (!W(XB_ITEM_FULL + (int)(k & 1), k >> 1)) return false;
-    idx = item_slot[k & 1];
-    arrive(XB_ITEM_EMPTY + (int)(k & 1));
-    return idx >= 0;
+  auto item_slot = [&](uint32_t k) -> WbItem& {
+    return *reinterpret_cast<WbItem*>(base + kWbOffItem + (int)(k & 1) * kWbItemBytes);
   };
+  // the k-th item has been decoded (false: no more); a reading warp gives it back when done
+  auto next_item = [&](uint32_t k) {
+    return W(XB_ITEM_FULL + (int)(k & 1), k >> 1) && !item_slot(k).end;
+  };
+  auto done_item = [&](uint32_t k) { arrive(XB_ITEM_EMPTY + (int)(k & 1)); };
   const int32_t tpt = 128 / a.R;             // tokens per query tile
   const float log2e = 1.4426950408889634f;
-  WbItem it;
 
-  if (warp >= 8) {
+  if (warp >= kWbCtl) {
     setmaxnreg_dec<kWbRegsControl>();
-    if (warp == 8) {
+    if (warp == kWbCtl) {
       // ---------------- scheduler, TMA ----------------
       if (lane == 0) {
         prefetch_tensormap(&tm_q);
@@ -323,6 +331,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       }
       uint32_t n = 0, ni = 0, issued[2] = {0, 0};   // streamed tiles, items with tiles
       bool ok = true;
+      WbItem it{};
       auto load = [&](uint8_t* dst, const CUtensorMap* tm, uint64_t* b, int32_t y, int32_t z) {
         tma_load_4d(dst, tm, b, 0, y, z, it.b);
         tma_load_4d(dst + 16384, tm, b, 64, y, z, it.b);
@@ -330,15 +339,16 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       for (uint32_t k = 0; ok; ++k) {
         if (k >= 2 && !W(XB_ITEM_EMPTY + (int)(k & 1), (k >> 1) - 1)) break;
         int32_t idx = 0;
+        if (lane == 0) idx = atomicAdd(p.counter, 1);
+        idx = __shfl_sync(0xffffffffu, idx, 0);
+        it.end = idx >= p.n_all;
+        if (!it.end) wb_item(it, p, idx);
         if (lane == 0) {
-          idx = atomicAdd(p.counter, 1);
-          if (idx >= p.n_all) idx = -1;
-          item_slot[k & 1] = idx;
+          item_slot(k) = it;
           mbar_arrive(bar + XB_ITEM_FULL + (int)(k & 1));
         }
-        idx = __shfl_sync(0xffffffffu, idx, 0);
-        if (idx < 0) break;
-        wb_item(it, p, idx);
+        __syncwarp();
+        if (it.end) break;
         if (it.nt == 0) continue;
         if (ni > 0 && !W(XB_STAY_EMPTY, ni - 1)) break;
         if (lane == 0) {
@@ -372,12 +382,11 @@ __global__ void __launch_bounds__(kWbThreads, 1)
             mbar_drain(bar + XB_STR_FULL + 2 * (int)(k & 1) + h, (k >> 1) & 1u, err);
         if (ni > 0) mbar_drain(bar + XB_STAY_FULL, (uint32_t)((ni - 1) & 1), err);
       }
-    } else if (warp == 9) {
+    } else if (warp == kWbCtl + 1) {
       // ---------------- S, dP ----------------
       constexpr uint32_t kIdT = idesc_bf16_f32(128, 128, 0);
       const uint32_t sa = smem_u32(base + kWbOffStay), str = smem_u32(base + kWbOffStream);
       uint32_t n = 0, ni = 0;                // tiles, items with tiles
-      int32_t idx;
       bool ok = true;
       // D = X Y^T of two 128 x 128 tiles in shared memory
       auto product = [&](uint32_t d, uint32_t xa, uint32_t ya) {
@@ -391,10 +400,10 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       // half h (Q or K; dO or V) of tile t (number m) has landed; its rows past the
       // sequence are cleared: they may hold anything, and their P and dS are 0, but
       // 0 * NaN is not.  (V needs none: a column of dP that nobody sees is dropped.)
-      auto landed = [&](int h, int32_t t, uint32_t m) {
+      auto landed = [&](const WbItem& it, int h, int32_t t, uint32_t m) {
         const int s = 2 * (int)(m & 1) + h;
         if (!W(XB_STR_FULL + s, m >> 1)) return false;
-        if (it.len < a.n_kv && (it.dkv || h == 0)) {
+        if (a.kv_len != nullptr && it.len < a.n_kv && (it.dkv || h == 0)) {
           const int32_t r0 = it.dkv
                                  ? (it.len - (int32_t)a.q_pos0 - (it.q_tile + t) * tpt) * a.R
                                  : it.len - win_key0(it.w, t);
@@ -403,8 +412,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         return true;
       };
       // S of tile t, into the buffer that tile m - 2 has left
-      auto issue_s = [&](int32_t t, uint32_t m) {
-        if (!landed(0, t, m)) return false;
+      auto issue_s = [&](const WbItem& it, int32_t t, uint32_t m) {
+        if (!landed(it, 0, t, m)) return false;
         if (m >= 2 && !W(XB_DONE + (int)(m & 1), (m >> 1) - 1)) return false;
         tc_fence_after();
         if (elect_one()) {
@@ -414,16 +423,15 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         __syncwarp();
         return true;
       };
-      for (uint32_t k = 0; ok && next_item(k, idx); ++k) {
-        wb_item(it, p, idx);
-        if (it.nt == 0) continue;
+      for (uint32_t k = 0; ok && next_item(k); ++k) {
+        const WbItem& it = item_slot(k);
         const bool dkv = it.dkv;
         const int32_t nt = it.nt;
-        ok = W(XB_STAY_FULL, ni) && issue_s(0, n);
+        if (nt > 0) ok = W(XB_STAY_FULL, ni) && issue_s(it, 0, n);
         if (!ok) break;
         for (int32_t t = 0; t < nt; ++t, ++n) {
           // dP over S, once that is in registers
-          if (!landed(1, t, n) || !W(XB_S_READ, n)) { ok = false; break; }
+          if (!landed(it, 1, t, n) || !W(XB_S_READ, n)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
             const uint32_t b = n & 1;
@@ -433,9 +441,10 @@ __global__ void __launch_bounds__(kWbThreads, 1)
             if (t + 1 == nt) umma_commit(bar + XB_STAY_EMPTY);
           }
           __syncwarp();
-          if (t + 1 < nt && !issue_s(t + 1, n + 1)) { ok = false; break; }
+          if (t + 1 < nt && !issue_s(it, t + 1, n + 1)) { ok = false; break; }
         }
-        ++ni;
+        if (nt > 0) ++ni;
+        if (ok) done_item(k);
       }
       // every MMA issued has finished before the tensor memory is freed
       if (elect_one()) {
@@ -443,26 +452,25 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         mbar_drain(bar + XB_DRAIN, 0, err);
       }
       __syncwarp();
-    } else if (warp == 10) {
+    } else if (warp == kWbCtl + 2) {
       // ---------------- dV, dK or dQ ----------------
       constexpr uint32_t kIdA = idesc_bf16_f32(128, 128, 1);
       const uint32_t str0 = smem_u32(base + kWbOffStream);
       uint32_t n = 0, ni = 0;
-      int32_t idx;
       bool ok = true;
-      // D (+)= X Y, X (bf16, two halves of 64) in TMEM, Y in shared memory
+      // D (+)= X Y, X (bf16, runs of 32 elements, 32 columns apart) in TMEM, Y in shared memory
       auto product = [&](uint32_t d, uint32_t x, uint32_t ya, bool add) {
         const uint64_t yd = smem_desc_sw128(ya, 16384, 1024);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          umma_bf16_ts(d, x + (kk >> 2) * 64 + (kk & 3) * 8, yd + kk * (2048 / 16), kIdA,
+          umma_bf16_ts(d, x + (kk >> 1) * 32 + (kk & 1) * 8, yd + kk * (2048 / 16), kIdA,
                        add || kk > 0 ? 1u : 0u);
       };
-      for (uint32_t k = 0; ok && next_item(k, idx); ++k) {
-        wb_item(it, p, idx);
-        if (it.nt == 0) continue;
-        const bool dkv = it.dkv;
-        const int32_t nt = it.nt;
+      for (uint32_t k = 0; ok && next_item(k); ++k) {
+        const bool dkv = item_slot(k).dkv;
+        const int32_t nt = item_slot(k).nt;
+        done_item(k);
+        if (nt == 0) continue;
         if (ni > 0 && !W(XB_ACC_EMPTY, ni - 1)) { ok = false; break; }
         for (int32_t t = 0; t < nt; ++t, ++n) {
           const uint32_t b = n & 1, str = str0 + b * 65536, x = tmem + 128 * b;
@@ -472,7 +480,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
           if (!W(XB_DS_FULL + (int)b, n >> 1)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
-            product(tmem + 384, x + 32, str, t > 0);
+            product(tmem + 384, x + 16, str, t > 0);
             umma_commit(bar + XB_STR_EMPTY + 2 * b);
             if (dkv) {
               product(tmem + 256, x, str + 32768, t > 0);
@@ -493,10 +501,9 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     } else {
       // ---------------- -lse log2 e and -D of the streamed query rows ----------------
       uint32_t n = 0;
-      int32_t idx;
       bool ok = true;
-      for (uint32_t k = 0; ok && next_item(k, idx); ++k) {
-        wb_item(it, p, idx);
+      for (uint32_t k = 0; ok && next_item(k); ++k) {
+        const WbItem& it = item_slot(k);
         for (int32_t t = 0; t < it.nt; ++t, ++n) {
           const int s = (int)(n & 1);
           if (n >= 2 && !W(XB_STR_EMPTY + 2 * s, (n >> 1) - 1)) { ok = false; break; }
@@ -514,55 +521,57 @@ __global__ void __launch_bounds__(kWbThreads, 1)
           }
           arrive(XB_META_FULL + s);
         }
+        if (ok) done_item(k);
       }
     }
   } else {
     setmaxnreg_inc<kWbRegsMath>();
     // ---------------- P, dS; outputs ----------------
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane, c0 = 64 * half;
+    const int wg = warp >> 2, row = (warp & 3) * 32 + lane, c0 = 32 * wg;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const float scale_log2 = a.scale * log2e;
     const uint64_t scale2 = pack_f32x2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
     const int64_t H = (int64_t)a.G * a.R;
     uint32_t n = 0, ni = 0;
-    int32_t idx;
     bool ok = true;
-    for (uint32_t k = 0; ok && next_item(k, idx); ++k) {
-      wb_item(it, p, idx);
+    for (uint32_t k = 0; ok && next_item(k); ++k) {
+      const WbItem& it = item_slot(k);
       // dq: this thread's query row
-      const int32_t i_row = it.dkv ? 0 : it.w.i0 + row / a.R;
-      const int32_t pos = it.dkv ? it.k0 + row : it.w.q_pos0 + i_row;   // key or query position
-      const int64_t qrow = ((int64_t)it.b * a.n_q + i_row) * H + (int64_t)it.g * a.R + row % a.R;
+      auto query = [&]() { return it.w.i0 + row / a.R; };
+      auto qrow = [&]() {
+        return ((int64_t)it.b * a.n_q + query()) * H + (int64_t)it.g * a.R + row % a.R;
+      };
+      // key (dk, dv) or query position
+      auto position = [&]() { return it.dkv ? it.k0 + row : it.w.q_pos0 + query(); };
       float nl = 0.f, nd = 0.f;
-      const bool row_live = !it.dkv && i_row < a.n_q && pos < it.len;
-      if (row_live) {
-        nl = -log2e * __ldg(a.lse + qrow);
-        nd = -__ldg(p.delta + qrow);
+      if (!it.dkv && query() < a.n_q && position() < it.len) {
+        nl = -log2e * __ldg(a.lse + qrow());
+        nd = -__ldg(p.delta + qrow());
       }
       const int32_t win = a.window > 0 ? (int32_t)min64(a.window, int64_t(1) << 30) : 1 << 30;
-      const int32_t sink = (int32_t)a.sink;
+      const int32_t sink = (int32_t)a.sink, nt = it.nt;
       // one tile; kDkv: lse and D come with the columns, P goes to the tensor core too.
-      // Of its 64 columns of the buffer, P takes the first 32, dS the others
-      auto tile = [&](auto kind, uint64_t vis) {
+      // Of its 32 columns of the buffer, P takes the first 16, dS the others
+      auto tile = [&](auto kind, uint32_t vis) {
         constexpr bool kDkv = decltype(kind)::value;
-        const bool full = __all_sync(0xffffffffu, vis == ~0ull);
-        const float* m = reinterpret_cast<const float*>(base + kWbOffMeta + (int)(n & 1) * 1024) +
-                         c0;
+        const bool full = __all_sync(0xffffffffu, vis == ~0u);
+        const ulonglong2* m = reinterpret_cast<const ulonglong2*>(
+            base + kWbOffMeta + (int)(n & 1) * 1024 + 4 * c0);
         const uint32_t ts = tmem + lane_base + 128 * (n & 1) + c0;
-        if (!W(XB_META_FULL + (int)(n & 1), n >> 1) || !W(XB_S_FULL, n)) return false;
+        if (kDkv && !W(XB_META_FULL + (int)(n & 1), n >> 1)) return false;
+        if (!W(XB_S_FULL, n)) return false;
         tc_fence_after();
-        uint32_t s[64], d[64];
-        tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(s));
-        tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+        uint32_t s[32];
+        tmem_ld_32x32b_x32(ts, s);
         tmem_ld_wait();
         tc_fence_before();
         arrive(XB_S_READ);
         const uint64_t nl2 = pack_f32x2(__float_as_uint(nl), __float_as_uint(nl));
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {        // columns c0 + 4 q .. + 3
+        for (int q = 0; q < 8; ++q) {         // columns c0 + 4 q .. + 3
           uint64_t l0 = nl2, l1 = nl2;
           if (kDkv) {
-            const ulonglong2 v = reinterpret_cast<const ulonglong2*>(m)[q];
+            const ulonglong2 v = m[q];
             l0 = v.x;
             l1 = v.y;
           }
@@ -575,70 +584,71 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         }
         if (!full) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
+          for (int c = 0; c < 32; ++c)
             if (!((vis >> c) & 1)) s[c] = 0u;
         }
         if (!W(XB_DP_FULL, n)) return false;
         tc_fence_after();
-        tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(d));
-        tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(d + 32));
+        // 16 columns of dP at a time: P takes the place of the first, dS of the second
+        uint32_t d[16], pk[16];
+        tmem_ld_32x32b_x16(ts, d);
         const uint64_t nd2 = pack_f32x2(__float_as_uint(nd), __float_as_uint(nd));
         tmem_ld_wait();
         if (kDkv) {
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-              pk[q] = pack_bf16x2(u2f(s[32 * cc + 2 * q]), u2f(s[32 * cc + 2 * q + 1]));
-            tmem_st_32x32b_x16(ts + 16 * cc, pk);
-          }
+          for (int q = 0; q < 16; ++q) pk[q] = pack_bf16x2(u2f(s[2 * q]), u2f(s[2 * q + 1]));
+          tmem_st_32x32b_x16(ts, pk);
         }
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
-          uint32_t pk[16];
+          if (cc == 1) {
+            tmem_ld_32x32b_x16(ts + 16, d);
+            tmem_ld_wait();
+          }
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
+          for (int q = 0; q < 4; ++q) {
             uint64_t d0 = nd2, d1 = nd2;
             if (kDkv) {
-              const ulonglong2 v = reinterpret_cast<const ulonglong2*>(m + 128)[8 * cc + q];
+              const ulonglong2 v = m[32 + 4 * cc + q];
               d0 = v.x;
               d1 = v.y;
             }
-            const int c = 32 * cc + 4 * q;
+            const int c = 16 * cc + 4 * q;
             float e[4];
             unpack_f32x2(mul_f32x2(pack_f32x2(s[c], s[c + 1]),
-                                   add_f32x2(pack_f32x2(d[c], d[c + 1]), d0)), e[0], e[1]);
+                                   add_f32x2(pack_f32x2(d[4 * q], d[4 * q + 1]), d0)), e[0], e[1]);
             unpack_f32x2(mul_f32x2(pack_f32x2(s[c + 2], s[c + 3]),
-                                   add_f32x2(pack_f32x2(d[c + 2], d[c + 3]), d1)), e[2], e[3]);
+                                   add_f32x2(pack_f32x2(d[4 * q + 2], d[4 * q + 3]), d1)), e[2],
+                         e[3]);
             if (!full) {                      // dO.v may be anything where nothing is seen
 #pragma unroll
               for (int i = 0; i < 4; ++i) e[i] = (vis >> (c + i)) & 1 ? e[i] : 0.f;
             }
-            pk[2 * q] = pack_bf16x2(e[0], e[1]);
-            pk[2 * q + 1] = pack_bf16x2(e[2], e[3]);
+            pk[8 * cc + 2 * q] = pack_bf16x2(e[0], e[1]);
+            pk[8 * cc + 2 * q + 1] = pack_bf16x2(e[2], e[3]);
           }
-          tmem_st_32x32b_x16(ts + 32 + 16 * cc, pk);
         }
+        tmem_st_32x32b_x16(ts + 16, pk);
         tmem_st_wait();
         tc_fence_before();
         arrive(XB_DS_FULL + (int)(n & 1));
         ++n;
         return true;
       };
-      // visible columns of this thread's 64, as bits
+      // visible columns of this thread's 32, as bits
       if (it.dkv) {                           // columns: rows of query tile q_tile + t
-        const bool sees_all = pos < sink;
+        const int32_t pos = position();
         int32_t d = pos - (int32_t)a.q_pos0 - it.q_tile * tpt;   // first query that sees the key
-        for (int32_t t = 0; ok && t < it.nt; ++t, d -= tpt) {
+        for (int32_t t = 0; ok && t < nt; ++t, d -= tpt) {
           const int32_t e = d + win;                             // first one past the window
           ok = tile(std::true_type{},
-                    range_bits(d > tpt ? 128 : d * a.R, sees_all || e > tpt ? 128 : e * a.R, c0));
+                    range_bits(d > tpt ? 128 : d * a.R, pos < sink || e > tpt ? 128 : e * a.R, c0));
         }
       } else {                                // columns: keys
-        for (int32_t t = 0; ok && t < it.nt; ++t) {
+        const int32_t pos = position();
+        for (int32_t t = 0; ok && t < nt; ++t) {
           const int32_t k0 = win_key0(it.w, t);
-          const uint64_t vis =
+          const uint32_t vis =
               t < it.w.ns
                   ? range_bits(0, it.w.s_end - k0, c0)
                   : range_bits(max(pos - win + 1 - k0, 0), min(pos - k0 + 1, 128), c0) |
@@ -647,50 +657,51 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         }
       }
       if (!ok) break;
-      // outputs: dk, dv items: warps 0-3 dV, 4-7 dK, a row of 128 each; dq: 64 columns each
-      const bool any = it.nt > 0;
+      // outputs: dk, dv items: warps 0-7 dV, 8-15 dK, 64 columns each; dq: 32 columns each
+      const bool any = nt > 0;
       if (any) {
         if (!W(XB_ACC_FULL, ni)) { ok = false; break; }
         tc_fence_after();
       }
-      const int ncol = it.dkv ? 4 : 2;        // groups of 32 columns
-      const uint32_t src =
-          tmem + lane_base + (it.dkv ? 256 + 128 * half : 384 + c0);
-      const float f = it.dkv && half == 0 ? 1.f : a.scale;
-      const bool live = any && (it.dkv ? pos < it.len : row_live);
-      const bool store = it.dkv ? pos < a.n_kv : i_row < a.n_q;
-      __nv_bfloat16* dst =
-          it.dkv ? (half == 0 ? a.dv : a.dk) +
-                       (((int64_t)it.b * a.G + it.g) * a.n_kv + pos) * kHeadDim
-                 : a.dq + qrow * kHeadDim + c0;
-      float* pdst = it.dkv && it.part >= 0
-                        ? p.part + (((int64_t)it.part * 2 + half) * 128 + row) * kHeadDim
-                        : nullptr;
+      const int ncol = it.dkv ? 4 : 2;        // groups of 16 columns
+      const int which = wg >> 1, oc = it.dkv ? 64 * (wg & 1) : c0;
+      const uint32_t src = tmem + lane_base + (it.dkv ? 256 + 128 * which : 384) + oc;
+      const float f = it.dkv && which == 0 ? 1.f : a.scale;
+      const int32_t pos = position();
+      const bool store = it.dkv ? pos < a.n_kv : query() < a.n_q;
+      const bool live = any && store && pos < it.len;
+      const bool part = it.dkv && it.part >= 0;
+      uint8_t* dst;
+      if (part)
+        dst = reinterpret_cast<uint8_t*>(
+            p.part + (((int64_t)it.part * 2 + which) * 128 + row) * kHeadDim + oc);
+      else if (it.dkv)
+        dst = reinterpret_cast<uint8_t*>(
+            (which == 0 ? a.dv : a.dk) +
+            (((int64_t)it.b * a.G + it.g) * a.n_kv + pos) * kHeadDim + oc);
+      else
+        dst = reinterpret_cast<uint8_t*>(a.dq + qrow() * kHeadDim + oc);
 #pragma unroll 1
       for (int cc = 0; cc < ncol; ++cc) {
-        uint32_t r[32];
+        uint32_t r[16];
         if (any) {
-          tmem_ld_32x32b_x32(src + 32 * cc, r);
+          tmem_ld_32x32b_x16(src + 16 * cc, r);
           tmem_ld_wait();
         }
 #pragma unroll
-        for (int q = 0; q < 32; ++q) r[q] = live ? __float_as_uint(f * u2f(r[q])) : 0u;
-        if (pdst != nullptr) {
+        for (int q = 0; q < 16; ++q) r[q] = live ? __float_as_uint(f * u2f(r[q])) : 0u;
+        float* o = reinterpret_cast<float*>(dst + cc * (part ? 64 : 32));
+        if (part) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            st_global_v8(pdst + 32 * cc + 8 * q, u2f(r[8 * q]), u2f(r[8 * q + 1]),
-                         u2f(r[8 * q + 2]), u2f(r[8 * q + 3]), u2f(r[8 * q + 4]),
-                         u2f(r[8 * q + 5]), u2f(r[8 * q + 6]), u2f(r[8 * q + 7]));
+          for (int q = 0; q < 2; ++q)
+            st_global_v8(o + 8 * q, u2f(r[8 * q]), u2f(r[8 * q + 1]), u2f(r[8 * q + 2]),
+                         u2f(r[8 * q + 3]), u2f(r[8 * q + 4]), u2f(r[8 * q + 5]),
+                         u2f(r[8 * q + 6]), u2f(r[8 * q + 7]));
         } else if (store) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              pk[q] = pack_bf16x2(u2f(r[16 * h + 2 * q]), u2f(r[16 * h + 2 * q + 1]));
-            st_global_v8(reinterpret_cast<float*>(dst + 32 * cc + 16 * h), u2f(pk[0]), u2f(pk[1]),
-                         u2f(pk[2]), u2f(pk[3]), u2f(pk[4]), u2f(pk[5]), u2f(pk[6]), u2f(pk[7]));
-          }
+          for (int q = 0; q < 8; ++q) r[q] = pack_bf16x2(u2f(r[2 * q]), u2f(r[2 * q + 1]));
+          st_global_v8(o, u2f(r[0]), u2f(r[1]), u2f(r[2]), u2f(r[3]), u2f(r[4]), u2f(r[5]),
+                       u2f(r[6]), u2f(r[7]));
         }
       }
       if (any) {
@@ -698,12 +709,13 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         arrive(XB_ACC_EMPTY);
         ++ni;
       }
+      done_item(k);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == kWbCtl + 1) tmem_dealloc(tmem, 512);
 }
 
 // dv, dk of the cut blocks: their chunks' sums added in chunk order, 4 values a
