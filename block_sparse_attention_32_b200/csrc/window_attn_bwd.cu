@@ -52,12 +52,13 @@ static_assert(kWbRegsControl + 4 * kWbRegsMath == 5 * kWbRegsAtLaunch,
               "warpgroup register shares must add up to the launch allocation");
 constexpr int kWbOffStay = 0;                          // K, V or Q, dO: 32 KB each
 constexpr int kWbOffStream = 65536;                    // two slots of 64 KB
-constexpr int kWbOffMeta = kWbOffStream + 2 * 65536;   // two slots: -lse log2 e [128], -D [128]
-constexpr int kWbOffBar = kWbOffMeta + 2 * 1024;
+constexpr int kWbOffMeta = kWbOffStream + 2 * 65536;   // slots of -lse log2 e [128], -D [128]
+constexpr int kWbMeta = 4;                             // fetched this many tiles ahead
+constexpr int kWbOffBar = kWbOffMeta + kWbMeta * 1024;
 enum {
   XB_ITEM_FULL = 0, XB_ITEM_EMPTY = 2, XB_STAY_FULL = 4, XB_STAY_EMPTY, XB_STR_FULL = 6,
-  XB_STR_EMPTY = 10, XB_META_FULL = 14, XB_DS_FULL = 16, XB_DONE = 18, XB_S_FULL = 20, XB_S_READ,
-  XB_DP_FULL, XB_ACC_FULL, XB_ACC_EMPTY, XB_DRAIN, XB_COUNT = XB_DRAIN + 2
+  XB_STR_EMPTY = 10, XB_DS_FULL = 14, XB_DONE = 16, XB_META_FULL = 18,
+  XB_META_EMPTY = XB_META_FULL + kWbMeta, XB_S_FULL = XB_META_EMPTY + kWbMeta, XB_S_READ, XB_DP_FULL, XB_ACC_FULL, XB_ACC_EMPTY, XB_DRAIN, XB_COUNT = XB_DRAIN + 2
 };
 constexpr int kWbOffMisc = kWbOffBar + XB_COUNT * 8;
 constexpr int kWbOffItem = (kWbOffMisc + 16 + 15) / 16 * 16;    // two slots
@@ -276,9 +277,12 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         mbar_init(bar + XB_STR_FULL + 2 * s + h, 1);
         mbar_init(bar + XB_STR_EMPTY + 2 * s + h, 1);
       }
-      mbar_init(bar + XB_META_FULL + s, 1);
       mbar_init(bar + XB_DS_FULL + s, 16);          // a lane of each warp
       mbar_init(bar + XB_DONE + s, 1);
+    }
+    for (int s = 0; s < kWbMeta; ++s) {
+      mbar_init(bar + XB_META_FULL + s, 1);
+      mbar_init(bar + XB_META_EMPTY + s, 16);
     }
     mbar_init(bar + XB_STAY_FULL, 1);
     mbar_init(bar + XB_STAY_EMPTY, 1);
@@ -500,24 +504,31 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       __syncwarp();
     } else {
       // ---------------- -lse log2 e and -D of the streamed query rows ----------------
-      uint32_t n = 0;
+      uint32_t n = 0;                        // tiles of dk, dv items
       bool ok = true;
       for (uint32_t k = 0; ok && next_item(k); ++k) {
         const WbItem& it = item_slot(k);
-        for (int32_t t = 0; t < it.nt; ++t, ++n) {
-          const int s = (int)(n & 1);
-          if (n >= 2 && !W(XB_STR_EMPTY + 2 * s, (n >> 1) - 1)) { ok = false; break; }
-          if (it.dkv) {
-            float* m = reinterpret_cast<float*>(base + kWbOffMeta + s * 1024);
-            for (int r = lane; r < 128; r += 32) {
-              const int64_t i = (int64_t)(it.q_tile + t) * tpt + r / a.R;
-              const bool live = i < a.n_q && a.q_pos0 + i < it.len;
-              const int64_t row =
-                  ((int64_t)it.b * a.n_q + i) * ((int64_t)a.G * a.R) + it.g * a.R + r % a.R;
-              // padding: p = 2^{0 - inf} = 0
-              m[r] = live ? -log2e * __ldg(a.lse + row) : -INFINITY;
-              m[128 + r] = live ? -__ldg(p.delta + row) : 0.f;
-            }
+        const int32_t nt = it.dkv ? it.nt : 0;
+        for (int32_t t = 0; t < nt; ++t, ++n) {
+          const int s = (int)(n % kWbMeta);
+          float v[4][2];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r = 32 * u + lane;
+            const int64_t i = (int64_t)(it.q_tile + t) * tpt + r / a.R;
+            const bool live = i < a.n_q && a.q_pos0 + i < it.len;
+            const int64_t row =
+                ((int64_t)it.b * a.n_q + i) * ((int64_t)a.G * a.R) + it.g * a.R + r % a.R;
+            // padding: p = 2^{0 - inf} = 0
+            v[u][0] = live ? -log2e * __ldg(a.lse + row) : -INFINITY;
+            v[u][1] = live ? -__ldg(p.delta + row) : 0.f;
+          }
+          if (n >= kWbMeta && !W(XB_META_EMPTY + s, n / kWbMeta - 1)) { ok = false; break; }
+          float* m = reinterpret_cast<float*>(base + kWbOffMeta + s * 1024);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            m[32 * u + lane] = v[u][0];
+            m[128 + 32 * u + lane] = v[u][1];
           }
           arrive(XB_META_FULL + s);
         }
@@ -532,7 +543,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     const float scale_log2 = a.scale * log2e;
     const uint64_t scale2 = pack_f32x2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
     const int64_t H = (int64_t)a.G * a.R;
-    uint32_t n = 0, ni = 0;
+    uint32_t n = 0, nm = 0, ni = 0;          // tiles, those of dk, dv items, items with tiles
     bool ok = true;
     for (uint32_t k = 0; ok && next_item(k); ++k) {
       const WbItem& it = item_slot(k);
@@ -556,9 +567,9 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         constexpr bool kDkv = decltype(kind)::value;
         const bool full = __all_sync(0xffffffffu, vis == ~0u);
         const ulonglong2* m = reinterpret_cast<const ulonglong2*>(
-            base + kWbOffMeta + (int)(n & 1) * 1024 + 4 * c0);
+            base + kWbOffMeta + (int)(nm % kWbMeta) * 1024 + 4 * c0);
         const uint32_t ts = tmem + lane_base + 128 * (n & 1) + c0;
-        if (kDkv && !W(XB_META_FULL + (int)(n & 1), n >> 1)) return false;
+        if (kDkv && !W(XB_META_FULL + (int)(nm % kWbMeta), nm / kWbMeta)) return false;
         if (!W(XB_S_FULL, n)) return false;
         tc_fence_after();
         uint32_t s[32];
@@ -632,6 +643,10 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         arrive(XB_DS_FULL + (int)(n & 1));
+        if (kDkv) {
+          arrive(XB_META_EMPTY + (int)(nm % kWbMeta));
+          ++nm;
+        }
         ++n;
         return true;
       };
