@@ -503,19 +503,20 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       }
       __syncwarp();
     } else {
-      // ---------------- -lse log2 e and -D of the streamed query rows ----------------
-      uint32_t n = 0;                        // tiles of dk, dv items
+      // ---------------- -lse log2 e and -D of the query rows: streamed (dk, dv), or the item's own (dq) ----------------
+      uint32_t n = 0;                        // slots filled: one per tile, or per dq item
       bool ok = true;
       for (uint32_t k = 0; ok && next_item(k); ++k) {
         const WbItem& it = item_slot(k);
-        const int32_t nt = it.dkv ? it.nt : 0;
+        const int32_t nt = it.dkv ? it.nt : min(it.nt, 1);
+        const int32_t q_tile = it.dkv ? it.q_tile : it.w.i0 / tpt;
         for (int32_t t = 0; t < nt; ++t, ++n) {
           const int s = (int)(n % kWbMeta);
           float v[4][2];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const int r = 32 * u + lane;
-            const int64_t i = (int64_t)(it.q_tile + t) * tpt + r / a.R;
+            const int64_t i = (int64_t)(q_tile + t) * tpt + r / a.R;
             const bool live = i < a.n_q && a.q_pos0 + i < it.len;
             const int64_t row =
                 ((int64_t)it.b * a.n_q + i) * ((int64_t)a.G * a.R) + it.g * a.R + r % a.R;
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     const float scale_log2 = a.scale * log2e;
     const uint64_t scale2 = pack_f32x2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
     const int64_t H = (int64_t)a.G * a.R;
-    uint32_t n = 0, nm = 0, ni = 0;          // tiles, those of dk, dv items, items with tiles
+    uint32_t n = 0, nm = 0, ni = 0;          // tiles, slots of lse and D, items with tiles
     bool ok = true;
     for (uint32_t k = 0; ok && next_item(k); ++k) {
       const WbItem& it = item_slot(k);
@@ -555,12 +556,18 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       // key (dk, dv) or query position
       auto position = [&]() { return it.dkv ? it.k0 + row : it.w.q_pos0 + query(); };
       float nl = 0.f, nd = 0.f;
-      if (!it.dkv && query() < a.n_q && position() < it.len) {
-        nl = -log2e * __ldg(a.lse + qrow());
-        nd = -__ldg(p.delta + qrow());
+      const int32_t nt = it.nt;
+      if (!it.dkv && nt > 0) {                // (padding rows: -inf, 0)
+        ok = W(XB_META_FULL + (int)(nm % kWbMeta), nm / kWbMeta);
+        const float* m =
+            reinterpret_cast<const float*>(base + kWbOffMeta + (int)(nm % kWbMeta) * 1024);
+        nl = m[row];
+        nd = m[128 + row];
+        arrive(XB_META_EMPTY + (int)(nm % kWbMeta));
+        ++nm;
       }
       const int32_t win = a.window > 0 ? (int32_t)min64(a.window, int64_t(1) << 30) : 1 << 30;
-      const int32_t sink = (int32_t)a.sink, nt = it.nt;
+      const int32_t sink = (int32_t)a.sink;
       // one tile; kDkv: lse and D come with the columns, P goes to the tensor core too.
       // Of its 32 columns of the buffer, P takes the first 16, dS the others
       auto tile = [&](auto kind, uint32_t vis) {
