@@ -125,10 +125,10 @@ def load_library(path: str) -> ctypes.CDLL:
     L.msa_paged_decode_attn.argtypes = [_PD, _I64, _I64, Tensor, _PC, _P, _P, _P,
                                         ctypes.c_size_t, _P, _P]
     L.msa_window_attn_fwd.argtypes = [_PD, _I64, _I64, Tensor, Tensor, Tensor, _P, _P, _P, _P,
-                                      _P]
+                                      _P, _P]
     L.msa_window_attn_bwd_workspace.argtypes = [_PD, _I64, _I64]
     L.msa_window_attn_bwd_workspace.restype = ctypes.c_size_t
-    L.msa_window_attn_bwd.argtypes = [_PD, _I64, _I64, Tensor, Tensor, Tensor, Tensor, Tensor,
+    L.msa_window_attn_bwd.argtypes = [_PD, _I64, _I64, Tensor, Tensor, Tensor, Tensor, _P, Tensor,
                                       _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]
     L.msa_debug_set_attn_wait_limit_ns.argtypes = [ctypes.c_uint64]
     L.msa_debug_set_attn_wait_limit_ns.restype = ctypes.c_uint64
@@ -427,10 +427,12 @@ def msa_paged_decode_attn(d: Dims, q, k_pages, v_pages, block_table, seq_lens, o
         raise MSAError("msa_paged_decode_attn", st)
 
 
-def msa_window_attn_fwd(d: Dims, window, n_sink, q, k, v, out, lse, kv_len=None, dev_err=None):
+def msa_window_attn_fwd(d: Dims, window, n_sink, q, k, v, out, lse, kv_len=None, out_rest=None,
+                        dev_err=None):
     """Sliding-window attention with sinks: q, out [B,n_q,H,128], k, v [B,G,n_kv,128]
-    bf16, lse [B,n_q,H] fp32, kv_len int32 [B] (padded batch) or None."""
-    st = calls().window_fwd(d, window, n_sink, q, k, v, out, lse, kv_len, dev_err)
+    bf16, lse [B,n_q,H] fp32, kv_len int32 [B] (padded batch) or None, out_rest int8 like
+    out (the bits behind it, for the backward) or None."""
+    st = calls().window_fwd(d, window, n_sink, q, k, v, out, out_rest, lse, kv_len, dev_err)
     if st:
         raise MSAError("msa_window_attn_fwd", st)
 
@@ -440,9 +442,10 @@ def msa_window_attn_bwd_workspace(d: Dims, window, n_sink) -> int:
 
 
 def msa_window_attn_bwd(d: Dims, window, n_sink, q, k, v, o, d_o, lse, dq, dk, dv, ws,
-                        kv_len=None, dev_err=None):
-    """dq [B,n_q,H,128], dk, dv [B,G,n_kv,128] (bf16) for the upstream d_o (bf16)."""
-    st = calls().window_bwd(d, window, n_sink, q, k, v, o, d_o, lse, dq, dk, dv, ws, kv_len,
+                        kv_len=None, o_rest=None, dev_err=None):
+    """dq [B,n_q,H,128], dk, dv [B,G,n_kv,128] (bf16) for the upstream d_o (bf16); o,
+    o_rest (or None) and lse as the forward left them."""
+    st = calls().window_bwd(d, window, n_sink, q, k, v, o, o_rest, d_o, lse, dq, dk, dv, ws, kv_len,
                             dev_err)
     if st:
         raise MSAError("msa_window_attn_bwd", st)

@@ -367,43 +367,46 @@ struct Window {
   }
 };
 
-// dims, window, n_sink, q, k, v, out, lse, kv_len, dev_err
+// dims, window, n_sink, q, k, v, out, out_rest, lse, kv_len, dev_err
 PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&] {
-    need_args(n, 10);
+    need_args(n, 11);
     Call c;
     const Window w(c, a);
     void* out = c.flat("out", a[6], w.qs, ScalarType::BFloat16, false);
-    float* lse = w.lse(c, a[7]);
-    int32_t* lens = w.lens(c, a[8]);
-    int32_t* err = c.dev_err(a[9]);
+    void* rest = c.flat("out_rest", a[7], w.qs, ScalarType::Char, true);
+    float* lse = w.lse(c, a[8]);
+    int32_t* lens = w.lens(c, a[9]);
+    int32_t* err = c.dev_err(a[10]);
     void* st = c.stream();
     return enqueue([&] {
-      return msa_window_attn_fwd(&w.d, w.window, w.sink, w.q, w.k, w.v, lens, out, lse, err, st);
+      return msa_window_attn_fwd(&w.d, w.window, w.sink, w.q, w.k, w.v, lens, out, rest, lse, err,
+                                 st);
     });
   });
 }
 
-// dims, window, n_sink, q, k, v, o, d_o, lse, dq, dk, dv, ws, kv_len, dev_err
+// dims, window, n_sink, q, k, v, o, o_rest, d_o, lse, dq, dk, dv, ws, kv_len, dev_err
 PyObject* window_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&] {
-    need_args(n, 15);
+    need_args(n, 16);
     Call c;
     const Window w(c, a);
     const msa_tensor o = c.rows("o", a[6], w.d.batch, w.d.n_q, w.d.h_q, MSA_HEAD_DIM);
-    const msa_tensor d_o = c.rows("d_o", a[7], w.d.batch, w.d.n_q, w.d.h_q, MSA_HEAD_DIM);
-    const float* lse = w.lse(c, a[8]);
-    void* dq = c.flat("dq", a[9], w.qs, ScalarType::BFloat16, false);
-    void* dk = c.flat("dk", a[10], w.ks, ScalarType::BFloat16, false);
-    void* dv = c.flat("dv", a[11], w.ks, ScalarType::BFloat16, false);
+    const void* rest = c.flat("o_rest", a[7], w.qs, ScalarType::Char, true);
+    const msa_tensor d_o = c.rows("d_o", a[8], w.d.batch, w.d.n_q, w.d.h_q, MSA_HEAD_DIM);
+    const float* lse = w.lse(c, a[9]);
+    void* dq = c.flat("dq", a[10], w.qs, ScalarType::BFloat16, false);
+    void* dk = c.flat("dk", a[11], w.ks, ScalarType::BFloat16, false);
+    void* dv = c.flat("dv", a[12], w.ks, ScalarType::BFloat16, false);
     size_t bytes;
-    void* ws = c.workspace(a[12], &bytes);
-    int32_t* lens = w.lens(c, a[13]);
-    int32_t* err = c.dev_err(a[14]);
+    void* ws = c.workspace(a[13], &bytes);
+    int32_t* lens = w.lens(c, a[14]);
+    int32_t* err = c.dev_err(a[15]);
     void* st = c.stream();
     return enqueue([&] {
-      return msa_window_attn_bwd(&w.d, w.window, w.sink, w.q, w.k, w.v, o, d_o, lse, lens, dq, dk,
-                                 dv, ws, bytes, err, st);
+      return msa_window_attn_bwd(&w.d, w.window, w.sink, w.q, w.k, w.v, o, rest, d_o, lse, lens, dq,
+                                 dk, dv, ws, bytes, err, st);
     });
   });
 }

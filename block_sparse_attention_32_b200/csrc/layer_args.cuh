@@ -105,14 +105,15 @@ struct PagedDecodeArgs {
 };
 
 struct WindowArgs {
-  const __nv_bfloat16 *q, *o, *d_o;   // q: [B, n_q, H, 128]; o, d_o: backward only
-  int64_t qs_b, qs_t, qs_h, os_b, os_t, os_h, ds_b, ds_t, ds_h;
+  const __nv_bfloat16 *o, *d_o;   // [B, n_q, H, 128], strided (backward)
+  int64_t os_b, os_t, os_h, ds_b, ds_t, ds_h;
   int64_t batch, n_q, n_kv, q_pos0;
   int64_t window, sink;           // visible: j <= t and (t - j < window or j < sink)
   int32_t G, R;
   float scale;
   const int32_t* kv_len;          // [B] or null: queries at positions >= kv_len are padding
   __nv_bfloat16* out;             // [B, n_q, H, 128]
+  int8_t* rest;                   // [B, n_q, H, 128] or null: the 8 bits behind out
   float* lse;                     // [B, n_q, H]
   __nv_bfloat16 *dq, *dk, *dv;    // backward
   int32_t* err;

@@ -927,19 +927,21 @@ msa_status msa_paged_decode_attn(const msa_dims* d, int64_t window, int64_t n_si
 
 msa_status msa_window_attn_fwd(const msa_dims* d, int64_t window, int64_t n_sink, msa_tensor q,
                                msa_tensor k, msa_tensor v, const int32_t* kv_len, void* out,
-                               float* lse, int32_t* dev_err, void* stream) {
+                               void* out_rest, float* lse, int32_t* dev_err, void* stream) {
   msa_status s = check_window(d, window, n_sink, kv_len);
   if (s != MSA_OK) return s;
   for (const msa_tensor* t : {&q, &k, &v})
     if ((s = check_tensor(*t)) != MSA_OK) return s;
   if (out == nullptr || lse == nullptr) return MSA_ERR_INVALID_ARG;
-  if (!aligned32(out) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return MSA_ERR_ALIGNMENT;
+  if (!aligned32(out) || !aligned16(out_rest) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return MSA_ERR_ALIGNMENT;
   CUtensorMap tq, tk, tv;
   if ((s = make_map_rows(&tq, d, q)) != MSA_OK) return s;
   if ((s = make_map_keys(&tk, d, k)) != MSA_OK) return s;
   if ((s = make_map_keys(&tv, d, v)) != MSA_OK) return s;
   msa::WindowArgs a = window_args(d, window, n_sink, kv_len, dev_err);
   a.out = reinterpret_cast<__nv_bfloat16*>(out);
+  a.rest = reinterpret_cast<int8_t*>(out_rest);
   a.lse = lse;
   return from_cuda(msa::launch_window_attn_fwd(tq, tk, tv, a,
                                                reinterpret_cast<cudaStream_t>(stream)));
@@ -951,8 +953,9 @@ size_t msa_window_attn_bwd_workspace(const msa_dims* d, int64_t window, int64_t 
 }
 
 msa_status msa_window_attn_bwd(const msa_dims* d, int64_t window, int64_t n_sink, msa_tensor q,
-                               msa_tensor k, msa_tensor v, msa_tensor o, msa_tensor d_o,
-                               const float* lse, const int32_t* kv_len, void* dq, void* dk,
+                               msa_tensor k, msa_tensor v, msa_tensor o,
+                               const void* o_rest, msa_tensor d_o, const float* lse,
+                               const int32_t* kv_len, void* dq, void* dk,
                                void* dv, void* ws, size_t ws_bytes, int32_t* dev_err,
                                void* stream) {
   msa_status s = check_window(d, window, n_sink, kv_len);
@@ -961,7 +964,7 @@ msa_status msa_window_attn_bwd(const msa_dims* d, int64_t window, int64_t n_sink
     if ((s = check_tensor(*t)) != MSA_OK) return s;
   if (lse == nullptr || dq == nullptr || dk == nullptr || dv == nullptr || ws == nullptr)
     return MSA_ERR_INVALID_ARG;
-  if (!aligned32(dq) || !aligned32(dk) || !aligned32(dv) || !aligned32(ws) ||
+  if (!aligned32(dq) || !aligned32(dk) || !aligned32(dv) || !aligned32(ws) || !aligned16(o_rest) ||
       (reinterpret_cast<uintptr_t>(lse) & 3u))
     return MSA_ERR_ALIGNMENT;
   const size_t need = msa_window_attn_bwd_workspace(d, window, n_sink);
@@ -981,6 +984,7 @@ msa_status msa_window_attn_bwd(const msa_dims* d, int64_t window, int64_t n_sink
   a.ds_b = d_o.s_batch;
   a.ds_t = d_o.s_tok;
   a.ds_h = d_o.s_head;
+  a.rest = const_cast<int8_t*>(reinterpret_cast<const int8_t*>(o_rest));
   a.lse = const_cast<float*>(lse);
   a.dq = reinterpret_cast<__nv_bfloat16*>(dq);
   a.dk = reinterpret_cast<__nv_bfloat16*>(dk);

@@ -59,6 +59,12 @@ enum {
 constexpr int kWaOffMisc = kWaOffBar + WB_COUNT * 8;
 constexpr int kWaSmemBytes = 1024 + kWaOffMisc + 16;
 static_assert(kWaSmemBytes <= 232448, "shared memory per block");
+// the 8 bits of x behind its bf16 rounding b (as fp32 bits): a signed count of 2^8
+// fp32 units from b
+__device__ __forceinline__ uint32_t rest_bits(float x, uint32_t b) {
+  const int32_t d = (int32_t)(__float_as_uint(x) - b);
+  return (uint32_t)max(-128, min(127, (d + 128) >> 8)) & 0xFFu;
+}
 constexpr float kLazyLog2 = 8.f;     // rescale O when a row's maximum grows by more than 2^8
 }  // namespace
 
@@ -446,7 +452,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         if (both) tmem_ld_32x32b_x16(to + 128 + 16 * cc, rb);
         tmem_ld_wait();
         if (store) {
-          uint32_t pk[8];
+          uint32_t pk[8], rest[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             float u = live ? u2f(r[2 * q]) * fa : 0.f, v = live ? u2f(r[2 * q + 1]) * fa : 0.f;
@@ -455,7 +461,13 @@ __global__ void __launch_bounds__(kWaThreads, 1)
               v += u2f(rb[2 * q + 1]) * fb;
             }
             pk[q] = pack_bf16x2(u, v);
+            if (a.rest != nullptr)
+              rest[q >> 1] |= (rest_bits(u, pk[q] << 16) | rest_bits(v, pk[q] & 0xFFFF0000u) << 8)
+                              << (16 * (q & 1));
           }
+          if (a.rest != nullptr)
+            *reinterpret_cast<uint4*>(a.rest + orow * kHeadDim + 16 * cc) =
+                make_uint4(rest[0], rest[1], rest[2], rest[3]);
           st_global_v8(reinterpret_cast<float*>(a.out + orow * kHeadDim + 16 * cc), u2f(pk[0]),
                        u2f(pk[1]), u2f(pk[2]), u2f(pk[3]), u2f(pk[4]), u2f(pk[5]), u2f(pk[6]),
                        u2f(pk[7]));

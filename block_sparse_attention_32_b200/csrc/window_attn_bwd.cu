@@ -176,7 +176,7 @@ __device__ __forceinline__ uint32_t range_bits(int32_t lo, int32_t hi, int32_t c
 }
 }  // namespace
 
-// D = dO.o of every row: 16 lanes of 16 bytes a row, 4 rows in flight a lane; the
+// D = dO.o of every row: 16 lanes of 8 features a row, 4 rows in flight a lane; the
 // last block lays out the cut key blocks and sets the item counter back
 constexpr int kWbPrepRows = 64;        // rows of a 256-thread block
 __global__ void __launch_bounds__(256)
@@ -190,22 +190,31 @@ __global__ void __launch_bounds__(256)
     const uint32_t r0 = blockIdx.x * kWbPrepRows + (threadIdx.x >> 4);
     const int c = 8 * (threadIdx.x & 15);
     uint4 ov[4], dv[4];
+    uint2 rv[4];                       // the 8 bits behind each o, when kept
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const uint32_t r = min(r0 + 16 * u, rows - 1);
       const uint32_t bt = r / H, h = r - bt * H, b = bt / n, t = bt - b * n;
       ov[u] = *reinterpret_cast<const uint4*>(a.o + b * a.os_b + t * a.os_t + h * a.os_h + c);
       dv[u] = *reinterpret_cast<const uint4*>(a.d_o + b * a.ds_b + t * a.ds_t + h * a.ds_h + c);
+      rv[u] = make_uint2(0u, 0u);
+      if (a.rest != nullptr)
+        rv[u] = *reinterpret_cast<const uint2*>(a.rest + (int64_t)r * kHeadDim + c);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const uint32_t x[4] = {ov[u].x, ov[u].y, ov[u].z, ov[u].w};
       const uint32_t y[4] = {dv[u].x, dv[u].y, dv[u].z, dv[u].w};
+      const uint32_t z[2] = {rv[u].x, rv[u].y};
+      // o as fp32 bits: (bf16 << 16) + (signed rest << 8)
+      auto rest = [&](int i) {
+        return (uint32_t)((int32_t)(z[i >> 2] << (24 - 8 * (i & 3))) >> 16) & 0xFFFFFF00u;
+      };
       float s = 0.f;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        s += u2f(x[q] << 16) * u2f(y[q] << 16) +
-             u2f(x[q] & 0xFFFF0000u) * u2f(y[q] & 0xFFFF0000u);
+        s += u2f((x[q] << 16) + rest(2 * q)) * u2f(y[q] << 16) +
+             u2f((x[q] & 0xFFFF0000u) + rest(2 * q + 1)) * u2f(y[q] & 0xFFFF0000u);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if ((lane & 15) == 0 && r0 + 16 * u < rows) delta[r0 + 16 * u] = s;

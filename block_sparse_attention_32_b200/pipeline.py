@@ -453,6 +453,7 @@ class WindowBuffers:
     dk: torch.Tensor | None = None
     dv: torch.Tensor | None = None
     ws: torch.Tensor | None = None
+    rest: torch.Tensor | None = None     # the 8 bits behind out, for the backward
 
     @staticmethod
     def allocate(d: capi.Dims, window=0, n_sink=0, backward=False,
@@ -472,6 +473,7 @@ class WindowBuffers:
             buf.dk = torch.empty(ks, dtype=torch.bfloat16, device=dev)
             buf.dv = torch.empty(ks, dtype=torch.bfloat16, device=dev)
             buf.ws = torch.empty(((n + 31) // 32 * 8,), dtype=torch.int32, device=dev)
+            buf.rest = torch.empty(qs, dtype=torch.int8, device=dev)
         return buf
 
 
@@ -480,7 +482,7 @@ def window_forward(buf: WindowBuffers, q, k, v, kv_len=None):
     kv_len int32 [B]: queries at positions >= kv_len[b] are padding (0, -inf).
     Returns (out, lse)."""
     capi.msa_window_attn_fwd(buf.dims, buf.window, buf.n_sink, q, k, v, buf.out, buf.lse, kv_len,
-                             buf.dev_err)
+                             buf.rest, buf.dev_err)
     return buf.out, buf.lse
 
 
@@ -490,5 +492,5 @@ def window_backward(buf: WindowBuffers, q, k, v, d_out, kv_len=None):
     if buf.ws is None:
         raise ValueError("allocate the WindowBuffers with backward=True")
     capi.msa_window_attn_bwd(buf.dims, buf.window, buf.n_sink, q, k, v, buf.out, d_out, buf.lse,
-                             buf.dq, buf.dk, buf.dv, buf.ws, kv_len, buf.dev_err)
+                             buf.dq, buf.dk, buf.dv, buf.ws, kv_len, buf.rest, buf.dev_err)
     return buf.dq, buf.dk, buf.dv

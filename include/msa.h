@@ -518,17 +518,22 @@ MSA_API msa_status msa_paged_decode_attn(const msa_dims* dims, int64_t window, i
  *          MSA_DEVERR_BAD_LENGTH and is clamped.
  *   out [B, n_q, h_q, 128] bf16 (32-byte aligned), lse [B, n_q, h_q] fp32,
  *   contiguous.  d_idx, h_kidx and q_window of dims have no meaning here.
+ *   out_rest  [B, n_q, h_q, 128] int8 (16-byte aligned), or NULL: the 8 bits behind
+ *          each bf16 of out, so that the fp32 with the bits (out << 16) + (rest << 8)
+ *          is o to 2^-17.  The backward's D = dO.o takes it: from the rounded out
+ *          alone D is off by up to 2^-9 sum |dO o|, which reaches dq and dk.
  * K and V must be finite at the keys below kv_len. */
 MSA_API msa_status msa_window_attn_fwd(const msa_dims* dims, int64_t window, int64_t n_sink,
                                        msa_tensor q, msa_tensor k, msa_tensor v,
-                                       const int32_t* kv_len, void* out, float* lse,
-                                       int32_t* dev_err, void* stream);
+                                       const int32_t* kv_len, void* out, void* out_rest,
+                                       float* lse, int32_t* dev_err, void* stream);
 
 /* Backward of msa_window_attn_fwd.  With p_j = e^{scale q.k_j - lse} over J(t),
  * D = dO.o and dS_j = p_j (dO.v_j - D):
  *   dq = scale sum_j dS_j k_j,  dk_j = scale sum dS_j q,  dv_j = sum p_j dO,
  * the last two over every (query, head of the group) that sees j.
- *   o, lse       the forward's results; d_o [B, n_q, h_q, 128] bf16
+ *   o, o_rest, lse  the forward's results (o_rest may be NULL: D from o alone);
+ *                d_o [B, n_q, h_q, 128] bf16
  *   dq           [B, n_q, h_q, 128] bf16, contiguous, 32-byte aligned
  *   dk, dv       [B, h_kv, n_kv, 128] bf16, contiguous, 32-byte aligned
  *   ws           msa_window_attn_bwd_workspace() bytes, 32-byte aligned
@@ -539,7 +544,8 @@ MSA_API size_t msa_window_attn_bwd_workspace(const msa_dims* dims, int64_t windo
                                              int64_t n_sink);
 MSA_API msa_status msa_window_attn_bwd(const msa_dims* dims, int64_t window, int64_t n_sink,
                                        msa_tensor q, msa_tensor k, msa_tensor v, msa_tensor o,
-                                       msa_tensor d_o, const float* lse, const int32_t* kv_len,
+                                       const void* o_rest, msa_tensor d_o, const float* lse,
+                                       const int32_t* kv_len,
                                        void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
                                        int32_t* dev_err, void* stream);
 

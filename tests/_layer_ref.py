@@ -7,7 +7,8 @@ here: a score is 128 exact bf16 products added in fp32, |score error| <=
 128 * 2^-24 * sum |q k| scale < 2^-14 for the tests' |q|, |k| of a few units, and
 a softmax weight's relative error is that of its exponent.
   attention   P is rounded to bf16 for P V (u sum p |v|), the result once (u |o|).
-  gradients   D = dO.o uses the rounded o, so |dD| <= sum |dO| (u |o| + u sum p |v|);
+  gradients   D = dO.o uses o as the forward left it: to 2^-17 with the kept bits, or
+              rounded to bf16, |dD| <= sum |dO| (u_o |o| + u sum p |v|), u_o = 2^-16 or u;
               P and dS are rounded once each for their products.
 All of these are worst cases per element; FRO bounds the relative Frobenius
 error, where the (at most three) roundings of an element add up like random
@@ -55,7 +56,7 @@ def attention(q, k, v, see, scale):
     return o, lse.T, bound, (p, av, q, kk, vv)
 
 
-def attention_grads(o, aux, d_o, see, scale, G):
+def attention_grads(o, aux, d_o, see, scale, G, u_o=2.0 ** -16):
     """dq, dk, dv of one sequence and their bounds."""
     p, av, q, kk, vv = aux
     H = q.shape[1]
@@ -63,7 +64,7 @@ def attention_grads(o, aux, d_o, see, scale, G):
     d_o = torch.where(see.any(1)[:, None, None], d_o.double(), torch.zeros_like(d_o.double()))
     dp = torch.einsum("ihd,hjd->hij", d_o, vv)
     D = (d_o * o).sum(-1).T                                           # [H, n_q]
-    eD = (d_o.abs() * (U * o.abs() + U * av)).sum(-1).T
+    eD = (d_o.abs() * (u_o * o.abs() + U * av)).sum(-1).T
     ds = p * (dp - D[..., None])
     adp = torch.einsum("ihd,hjd->hij", d_o.abs(), vv.abs())
     eds = U * ds.abs() + p * (eD[..., None] * (1 + U) + SMALL * (adp + D.abs()[..., None]))

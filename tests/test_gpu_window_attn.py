@@ -103,6 +103,44 @@ def test_backward(case):
         assert torch.equal(x, y)                      # no order of sums is left to chance
 
 
+def test_backward_without_the_kept_bits():
+    """o alone gives D to bf16: wider bounds, the same otherwise."""
+    case = CASES[6]
+    B, n_q, n_kv, pos0, H, G, W, S, lens = case
+    q, k, v, d_o, _ = _inputs(case)
+    buf = pipeline.WindowBuffers.allocate(pipeline.window_dims(B, n_q, n_kv, pos0, H, G), W, S,
+                                          backward=True)
+    buf.rest = None
+    pipeline.window_forward(buf, q, k, v)
+    dq, dk, dv = pipeline.window_backward(buf, q, k, v, d_o)
+    scale = 1 / math.sqrt(128)
+    for b in range(B):
+        see = ref.visible(n_q, n_kv, pos0, W, S, n_kv, "cuda")
+        o, lse, bound, aux = ref.attention(q[b], k[b], v[b], see, scale)
+        (eq, bq), (ek, bk), (ev, bv) = ref.attention_grads(o, aux, d_o[b], see, scale, G, ref.U)
+        ref.close("dq", dq[b], eq, bq)
+        ref.close("dk", dk[b], ek, bk)
+        ref.close("dv", dv[b], ev, bv)
+
+
+@pytest.mark.parametrize("case", [CASES[6], CASES[11]], ids=str)
+def test_kept_bits_extend_the_output(case):
+    """out and its kept bits together are o up to the rounding of P and fp32."""
+    B, n_q, n_kv, pos0, H, G, W, S, lens = case
+    q, k, v, d_o, kv_len = _inputs(case)
+    buf = pipeline.WindowBuffers.allocate(pipeline.window_dims(B, n_q, n_kv, pos0, H, G), W, S,
+                                          backward=True)
+    buf.rest.fill_(99)
+    out, _ = pipeline.window_forward(buf, q, k, v, kv_len)
+    bits = (out.view(torch.int16).int() << 16) + (buf.rest.int() << 8)
+    full = bits.view(torch.float32)
+    # the 8 bits leave half a unit of 2^-16 relative, and keep out as the nearest bf16
+    assert ((full - out.float()).abs() <= 2.0 ** -8 * out.float().abs() + 1e-38).all()
+    for b, o, l, bound, _ in _expect(case, q, k, v, d_o, 1 / math.sqrt(128)):
+        rounded_p = bound - ref.U * o.abs()          # what is left without the rounding of o
+        ref.close("full", full[b], o, rounded_p + 2.0 ** -15 * o.abs())
+
+
 def test_scale_and_strided_views():
     """q, k, v as views of one token-major projection; d_o with heads outermost; a
     scale of its own."""
