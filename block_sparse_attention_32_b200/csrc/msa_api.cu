@@ -69,10 +69,12 @@ int32_t paged_decode_tile();
 cudaError_t launch_paged_decode(const CUtensorMap&, const CUtensorMap&, PagedDecodeArgs, void*,
                                 cudaStream_t);
 cudaError_t launch_window_attn_fwd(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
-                                   const WindowArgs&, cudaStream_t);
+                                   const CUtensorMap&, const CUtensorMap&, const WindowArgs&,
+                                   cudaStream_t);
 size_t window_attn_bwd_workspace(const WindowArgs&);   // 0: too many work items
 cudaError_t launch_window_attn_bwd(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
-                                   const CUtensorMap&, WindowArgs, void*, cudaStream_t);
+                                   const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                   WindowArgs, void*, cudaStream_t);
 cudaError_t launch_merge(const int32_t*, const float*, const void*, bool, void*, float*,
                          int64_t, int64_t, int32_t, int32_t, int64_t, int32_t*, cudaStream_t);
 }  // namespace msa
@@ -762,10 +764,11 @@ msa_status make_map_rows(CUtensorMap* map, const msa_dims* d, const msa_tensor& 
   return make_map(map, t.ptr, MSA_HEAD_DIM, d->h_q, d->n_q, d->batch, t.s_head, t.s_tok,
                   t.s_batch, (uint32_t)R, (uint32_t)(MSA_BLOCK_TOKENS / R));
 }
-// k, v [B, h_kv, n_kv, 128]: 128 keys, 64 columns a box
-msa_status make_map_keys(CUtensorMap* map, const msa_dims* d, const msa_tensor& t) {
+// k, v [B, h_kv, n_kv, 128]: `keys` keys, 64 columns a box
+msa_status make_map_keys(CUtensorMap* map, const msa_dims* d, const msa_tensor& t,
+                         uint32_t keys) {
   return make_map(map, t.ptr, MSA_HEAD_DIM, d->n_kv, d->h_kv, d->batch, t.s_tok, t.s_head,
-                  t.s_batch, MSA_BLOCK_TOKENS, 1);
+                  t.s_batch, keys, 1);
 }
 
 msa_status check_window(const msa_dims* d, int64_t window, int64_t n_sink,
@@ -935,15 +938,17 @@ msa_status msa_window_attn_fwd(const msa_dims* d, int64_t window, int64_t n_sink
   if (out == nullptr || lse == nullptr) return MSA_ERR_INVALID_ARG;
   if (!aligned32(out) || !aligned16(out_rest) || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return MSA_ERR_ALIGNMENT;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, tk32, tv32;
   if ((s = make_map_rows(&tq, d, q)) != MSA_OK) return s;
-  if ((s = make_map_keys(&tk, d, k)) != MSA_OK) return s;
-  if ((s = make_map_keys(&tv, d, v)) != MSA_OK) return s;
+  if ((s = make_map_keys(&tk, d, k, 128)) != MSA_OK) return s;
+  if ((s = make_map_keys(&tv, d, v, 128)) != MSA_OK) return s;
+  if ((s = make_map_keys(&tk32, d, k, 32)) != MSA_OK) return s;
+  if ((s = make_map_keys(&tv32, d, v, 32)) != MSA_OK) return s;
   msa::WindowArgs a = window_args(d, window, n_sink, kv_len, dev_err);
   a.out = reinterpret_cast<__nv_bfloat16*>(out);
   a.rest = reinterpret_cast<int8_t*>(out_rest);
   a.lse = lse;
-  return from_cuda(msa::launch_window_attn_fwd(tq, tk, tv, a,
+  return from_cuda(msa::launch_window_attn_fwd(tq, tk, tv, tk32, tv32, a,
                                                reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -970,11 +975,13 @@ msa_status msa_window_attn_bwd(const msa_dims* d, int64_t window, int64_t n_sink
   const size_t need = msa_window_attn_bwd_workspace(d, window, n_sink);
   if (need == 0) return MSA_ERR_UNSUPPORTED;
   if (ws_bytes < need) return MSA_ERR_WORKSPACE_TOO_SMALL;
-  CUtensorMap tq, tdo, tk, tv;
+  CUtensorMap tq, tdo, tk, tv, tk32, tv32;
   if ((s = make_map_rows(&tq, d, q)) != MSA_OK) return s;
   if ((s = make_map_rows(&tdo, d, d_o)) != MSA_OK) return s;
-  if ((s = make_map_keys(&tk, d, k)) != MSA_OK) return s;
-  if ((s = make_map_keys(&tv, d, v)) != MSA_OK) return s;
+  if ((s = make_map_keys(&tk, d, k, 128)) != MSA_OK) return s;
+  if ((s = make_map_keys(&tv, d, v, 128)) != MSA_OK) return s;
+  if ((s = make_map_keys(&tk32, d, k, 32)) != MSA_OK) return s;
+  if ((s = make_map_keys(&tv32, d, v, 32)) != MSA_OK) return s;
   msa::WindowArgs a = window_args(d, window, n_sink, kv_len, dev_err);
   a.o = reinterpret_cast<const __nv_bfloat16*>(o.ptr);
   a.os_b = o.s_batch;
@@ -989,7 +996,7 @@ msa_status msa_window_attn_bwd(const msa_dims* d, int64_t window, int64_t n_sink
   a.dq = reinterpret_cast<__nv_bfloat16*>(dq);
   a.dk = reinterpret_cast<__nv_bfloat16*>(dk);
   a.dv = reinterpret_cast<__nv_bfloat16*>(dv);
-  return from_cuda(msa::launch_window_attn_bwd(tq, tdo, tk, tv, a, ws,
+  return from_cuda(msa::launch_window_attn_bwd(tq, tdo, tk, tv, tk32, tv32, a, ws,
                                                reinterpret_cast<cudaStream_t>(stream)));
 }
 

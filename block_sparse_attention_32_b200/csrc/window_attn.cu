@@ -54,10 +54,13 @@ constexpr int kWaOffBar = kWaOffML + 1024;
 enum {
   WB_Q_FULL = 0, WB_Q_EMPTY = 2, WB_S_FULL = 4, WB_P_FULL = 6, WB_PV_DONE = 8, WB_O_EMPTY = 10,
   WB_S_READ = 12, WB_JOIN, WB_KV_FULL, WB_KV_EMPTY = WB_KV_FULL + kWaRing,
-  WB_DRAIN = WB_KV_EMPTY + kWaRing, WB_COUNT = WB_DRAIN + 2
+  WB_DRAIN = WB_KV_EMPTY + kWaRing, WB_ITEM_FULL = WB_DRAIN + 2, WB_ITEM_EMPTY = WB_ITEM_FULL + 2,
+  WB_COUNT = WB_ITEM_EMPTY + 2
 };
 constexpr int kWaOffMisc = kWaOffBar + WB_COUNT * 8;
-constexpr int kWaSmemBytes = 1024 + kWaOffMisc + 16;
+constexpr int kWaOffItem = kWaOffMisc + 16;              // two slots
+constexpr int kWaSmemBytes = 1024 + kWaOffItem + 2 * (int)sizeof(WinItem);
+constexpr int kWaItemReaders = 10;                      // warps 0-7, 9, 10
 static_assert(kWaSmemBytes <= 232448, "shared memory per block");
 // the 8 bits of x behind its bf16 rounding b (as fp32 bits): a signed count of 2^8
 // fp32 units from b
@@ -72,6 +75,8 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     window_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                            const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v,
+                           const __grid_constant__ CUtensorMap tm_k32,
+                           const __grid_constant__ CUtensorMap tm_v32,
                            const __grid_constant__ WindowArgs a, int32_t tiles_per_item,
                            int32_t n_items) {
   extern __shared__ uint8_t smem_raw[];
@@ -100,6 +105,10 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     mbar_init(bar + WB_JOIN, 4);
     mbar_init(bar + WB_DRAIN, 1);
     mbar_init(bar + WB_DRAIN + 1, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar + WB_ITEM_FULL + s, 1);
+      mbar_init(bar + WB_ITEM_EMPTY + s, kWaItemReaders);
+    }
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -121,18 +130,30 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     if (lane == 0) mbar_arrive(bar + id);
   };
   const bool split = tiles_per_item == 1;              // the halves share one row tile
-  WinItem it{};
+  // Items are decoded once, by the TMA warp, and kept in shared memory: the softmax
+  // warps need their registers.  `cur`: the role's item
+  auto item_slot = [&](uint32_t k) {
+    return reinterpret_cast<WinItem*>(base + kWaOffItem) + (k & 1);
+  };
+  const WinItem* cur = item_slot(0);
+  auto next_item = [&](uint32_t k) {
+    if (!W(WB_ITEM_FULL + (int)(k & 1), k >> 1)) return false;
+    cur = item_slot(k);
+    return cur->nt >= 0;                               // -1: there are no more
+  };
+  auto done_item = [&](uint32_t k) { arrive(WB_ITEM_EMPTY + (int)(k & 1)); };
   // step i of an item is key tile tile_of(i) of half i & 1; does the half need it?
-  auto n_steps = [&]() { return split ? it.nt : 2 * it.nt; };
+  auto n_steps = [&]() { return split ? cur->nt : 2 * cur->nt; };
   auto tile_of = [&](int i) { return split ? i : i >> 1; };
   auto takes = [&](int i) {
-    if (split) return i < it.nt;
+    if (split) return i < cur->nt;
     const int j = i >> 1;
-    return (i & 1) ? it.rows[1] && j < it.nt && (j < it.ns || j >= it.beg_b) : j <= it.end_a;
+    return (i & 1) ? cur->rows[1] && j < cur->nt && (4 * j < cur->nc || j >= cur->beg_b)
+                   : j <= cur->end_a;
   };
   // ring slots of an item's tiles, in the order K0 K1 V0 K2 V1 ... (counted from its first)
   auto slot_k = [&](int j) { return (uint32_t)(j == 0 ? 0 : 2 * j - 1); };
-  auto slot_v = [&](int j) { return (uint32_t)(j == it.nt - 1 ? 2 * j + 1 : 2 * j + 2); };
+  auto slot_v = [&](int j) { return (uint32_t)(j == cur->nt - 1 ? 2 * j + 1 : 2 * j + 2); };
 
   if (warp >= 8) {
     setmaxnreg_dec<kWaRegsControl>();
@@ -144,21 +165,31 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       prefetch_tensormap(&tm_v);
     }
     uint32_t nq[2] = {0, 0}, n = 0;          // Q loads per tile, ring slots
+    WinItem it{};
     bool ok = true;
-    auto push = [&](const CUtensorMap* tm, int32_t key0) {
+    auto push = [&](const CUtensorMap* tm, const CUtensorMap* tm32, int j) {
       const uint32_t s = n % kWaRing;
       if (n >= kWaRing && !W(WB_KV_EMPTY + s, n / kWaRing - 1)) return false;
       if (lane == 0) {
         uint8_t* dst = base + kWaOffRing + s * 32768;
         mbar_arrive_expect_tx(bar + WB_KV_FULL + s, 32768u);
-        tma_load_4d(dst, tm, bar + WB_KV_FULL + s, 0, key0, it.g, it.b);
-        tma_load_4d(dst + 16384, tm, bar + WB_KV_FULL + s, 64, key0, it.g, it.b);
+        win_load_keys(dst, tm, tm32, bar + WB_KV_FULL + s, it, j);
       }
       ++n;
       return true;
     };
-    for (int32_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-      win_item(it, a, i, tiles_per_item);
+    for (uint32_t k = 0; ok; ++k) {
+      const int32_t i = (int32_t)(blockIdx.x + k * gridDim.x);
+      if (k >= 2 && !W(WB_ITEM_EMPTY + (int)(k & 1), (k >> 1) - 1)) break;
+      const bool end = i >= n_items;
+      if (!end) win_item(it, a, i, tiles_per_item);
+      if (lane == 0) {
+        *item_slot(k) = it;
+        if (end) item_slot(k)->nt = -1;
+        mbar_arrive(bar + WB_ITEM_FULL + (int)(k & 1));
+      }
+      __syncwarp();
+      if (end) break;
       for (int x = 0; ok && x < 2; ++x) {
         if (!it.rows[x]) continue;
         ok = nq[x] == 0 || W(WB_Q_EMPTY + x, nq[x] - 1);
@@ -171,9 +202,9 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         }
         if (ok) ++nq[x];
       }
-      if (ok && it.nt > 0) ok = push(&tm_k, win_key0(it, 0));
+      if (ok && it.nt > 0) ok = push(&tm_k, &tm_k32, 0);
       for (int j = 0; ok && j < it.nt; ++j)
-        ok = (j + 1 == it.nt || push(&tm_k, win_key0(it, j + 1))) && push(&tm_v, win_key0(it, j));
+        ok = (j + 1 == it.nt || push(&tm_k, &tm_k32, j + 1)) && push(&tm_v, &tm_v32, j);
     }
     // no copy may still be writing shared memory when the block exits
     if (lane == 0) {
@@ -188,8 +219,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     const uint32_t ring = smem_u32(base + kWaOffRing), qs = smem_u32(base + kWaOffQ);
     uint32_t nq[2] = {0, 0}, ns = 0, n0 = 0;     // Q tiles used, S products, ring slots
     bool ok = true;
-    for (int32_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-      win_item(it, a, i, tiles_per_item);
+    for (uint32_t ki = 0; ok && next_item(ki); ++ki) {
       bool seen_q[2] = {false, false};
       const int n_st = n_steps();
       int left = 0;                          // products still to come
@@ -219,7 +249,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           if (split || x == 1 || !takes(k + 1)) umma_commit(bar + WB_KV_EMPTY + slot);
           if (left == 0) {
             umma_commit(bar + WB_Q_EMPTY);
-            if (it.rows[1]) umma_commit(bar + WB_Q_EMPTY + 1);
+            if (cur->rows[1]) umma_commit(bar + WB_Q_EMPTY + 1);
           }
         }
         __syncwarp();
@@ -228,9 +258,10 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         issue(std::integral_constant<int, 0>{}, k);
         issue(std::integral_constant<int, 1>{}, k + 1);
       }
-      n0 += 2 * (uint32_t)it.nt;
+      n0 += 2 * (uint32_t)cur->nt;
       for (int x = 0; x < 2; ++x)
-        if (it.rows[x]) ++nq[x];
+        if (cur->rows[x]) ++nq[x];
+      if (ok) done_item(ki);
     }
     // every MMA issued has finished before the tensor memory is freed
     if (elect_one()) {
@@ -243,8 +274,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     constexpr uint32_t kIdO = idesc_bf16_f32(128, 128, 1);
     uint32_t np[2] = {0, 0}, no[2] = {0, 0}, n0 = 0;     // products, items with an O, ring slots
     bool ok = true;
-    for (int32_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-      win_item(it, a, i, tiles_per_item);
+    for (uint32_t ki = 0; ok && next_item(ki); ++ki) {
       bool begun[2] = {false, false};
       const int n_st = n_steps();
       auto issue = [&](auto half, int k) {
@@ -257,8 +287,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           if (!W(WB_KV_FULL + slot, sv / kWaRing)) { ok = false; return; }
           // keys past the sequence's end may hold anything: their V rows are cleared
           // (P is 0 there, and 0 * NaN would not be)
-          const int32_t k0 = win_key0(it, j);
-          if (it.len < a.n_kv && k0 + 128 > it.len) win_clear_rows(tile, it.len - k0, lane);
+          if (a.kv_len != nullptr && cur->len < a.n_kv) win_clear_keys(tile, *cur, j, lane);
         }
         if (!begun[x] && no[x] > 0 && !W(WB_O_EMPTY + x, no[x] - 1)) { ok = false; return; }
         if (!W(WB_P_FULL + x, np[x])) { ok = false; return; }
@@ -280,9 +309,10 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         issue(std::integral_constant<int, 0>{}, k);
         issue(std::integral_constant<int, 1>{}, k + 1);
       }
-      n0 += 2 * (uint32_t)it.nt;
+      n0 += 2 * (uint32_t)cur->nt;
       for (int x = 0; x < 2; ++x)
         if (begun[x]) ++no[x];
+      if (ok) done_item(ki);
     }
     if (elect_one()) {
       umma_commit(bar + WB_DRAIN + 1);
@@ -300,11 +330,12 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     const float scale_log2 = a.scale * 1.4426950408889634f;
     const uint64_t scale2 = pack_f32x2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
     const int32_t tpt = 128 / a.R;            // tokens per row tile
+    const int32_t sink = (int32_t)a.sink;
     float2* ml_b = reinterpret_cast<float2*>(base + kWaOffML);
     uint32_t ns = 0, np = 0, np_other = 0, nj = 0;
     bool ok = true;
-    for (int32_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-      win_item(it, a, i, tiles_per_item);
+    for (uint32_t ki = 0; ok && next_item(ki); ++ki) {
+      const WinItem& it = *cur;
       const int32_t first = it.i0 + (split ? 0 : x * tpt);       // the row tile's first query
       const int32_t i_row = first + row / a.R;
       const int32_t t = it.q_pos0 + i_row;
@@ -318,7 +349,6 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         if (!W(WB_S_FULL + x, ns)) { ok = false; break; }
         ++ns;
         tc_fence_after();
-        const int32_t k0 = win_key0(it, j);
         uint32_t s[128];
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc)
@@ -326,24 +356,20 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         tmem_ld_wait();
         tc_fence_before();
         arrive(WB_S_READ);
-        // visible columns c: c <= hi and (c >= lo or c < sk)
-        int32_t hi, lo, sk;
-        bool full;
-        if (j < it.ns) {                      // a tile of sinks before the window
-          hi = it.s_end - 1 - k0;
-          lo = 0;
-          sk = 0;
-          full = hi >= 127;
-        } else {
-          hi = t - k0;
-          lo = t - it.W + 1 - k0;
-          sk = (int32_t)min64(max64(a.sink - k0, 0), 128);
-          full = k0 + 127 <= t_min && (t_max - it.W + 1 <= k0 || sk >= 128);
-        }
+        // is every column visible to every row of the warp?
+        const int32_t k0 = win_chunk(it, 4 * j);
+        const bool full = !win_mixed(it, j) &&
+                          (4 * j < it.nc ? k0 + 128 <= it.s_end
+                                         : k0 + 127 <= t_min && (t_max - it.W + 1 <= k0 ||
+                                                                 sink - k0 >= 128));
         if (!full) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (!(c <= hi && (c >= lo || c < sk))) s[c] = 0xFF800000u;   // -inf
+          for (int cc = 0; cc < 4; ++cc) {
+            const uint32_t vis = win_visible(it, 4 * j + cc, t, sink);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((vis >> c) & 1)) s[32 * cc + c] = 0xFF800000u;   // -inf
+          }
         }
         float mq[4];                          // four chains: the latency of one is 64 steps
 #pragma unroll
@@ -421,6 +447,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         if (x == 1) {
           ml_b[row] = make_float2(m, l);
           arrive(WB_JOIN);
+          done_item(ki);
           continue;                            // A frees B's accumulators
         }
         if (!W(WB_JOIN, nj)) { ok = false; break; }
@@ -476,6 +503,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       tc_fence_before();
       if (begun) arrive(WB_O_EMPTY + x);
       if (both) arrive(WB_O_EMPTY + 1);
+      done_item(ki);
     }
   }
   tc_fence_before();
@@ -485,7 +513,8 @@ __global__ void __launch_bounds__(kWaThreads, 1)
 }
 
 cudaError_t launch_window_attn_fwd(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                                   const CUtensorMap& tm_v, const WindowArgs& a,
+                                   const CUtensorMap& tm_v, const CUtensorMap& tm_k32,
+                                   const CUtensorMap& tm_v32, const WindowArgs& a,
                                    cudaStream_t st) {
   static KernelSetup setup;
   int sms = 0;
@@ -499,7 +528,7 @@ cudaError_t launch_window_attn_fwd(const CUtensorMap& tm_q, const CUtensorMap& t
   const int64_t items = a.batch * a.G * ((tiles + per - 1) / per);
   if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
   window_attn_fwd_kernel<<<(unsigned)min64(items, sms), kWaThreads, kWaSmemBytes, st>>>(
-      tm_q, tm_k, tm_v, a, per, (int32_t)items);
+      tm_q, tm_k, tm_v, tm_k32, tm_v32, a, per, (int32_t)items);
   return cudaGetLastError();
 }
 

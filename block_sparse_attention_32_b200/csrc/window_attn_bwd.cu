@@ -167,13 +167,6 @@ __device__ __forceinline__ void wb_item(WbItem& it, const WindowBwdArgs& p, int3
   }
 }
 
-// columns lo .. hi - 1 of the 32 from c0 on, as bits
-__device__ __forceinline__ uint32_t range_bits(int32_t lo, int32_t hi, int32_t c0) {
-  lo = max(lo - c0, 0);
-  hi = min(hi - c0, 32);
-  if (lo >= hi) return 0u;
-  return (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
-}
 }  // namespace
 
 // D = dO.o of every row: 16 lanes of 8 features a row, 4 rows in flight a lane; the
@@ -267,6 +260,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
                            const __grid_constant__ CUtensorMap tm_do,
                            const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v,
+                           const __grid_constant__ CUtensorMap tm_k32,
+                           const __grid_constant__ CUtensorMap tm_v32,
                            const __grid_constant__ WindowBwdArgs p) {
   extern __shared__ uint8_t smem_raw[];
   // (an offset, so that the compiler still knows the address space)
@@ -372,16 +367,18 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         }
         ++ni;
         for (int32_t t = 0; t < it.nt; ++t, ++n) {
-          const int32_t y = it.dkv ? it.g * a.R : win_key0(it.w, t);
-          const int32_t z = it.dkv ? (it.q_tile + t) * tpt : it.g;
           for (int h = 0; ok && h < 2; ++h) {
             const int s = 2 * (int)(n & 1) + h;
             ok = n < 2 || W(XB_STR_EMPTY + s, (n >> 1) - 1);
             if (ok && lane == 0) {
               mbar_arrive_expect_tx(bar + XB_STR_FULL + s, 32768u);
-              load(base + kWbOffStream + s * 32768,
-                   it.dkv ? (h ? &tm_do : &tm_q) : (h ? &tm_v : &tm_k), bar + XB_STR_FULL + s, y,
-                   z);
+              uint8_t* dst = base + kWbOffStream + s * 32768;
+              if (it.dkv)
+                load(dst, h ? &tm_do : &tm_q, bar + XB_STR_FULL + s, it.g * a.R,
+                     (it.q_tile + t) * tpt);
+              else
+                win_load_keys(dst, h ? &tm_v : &tm_k, h ? &tm_v32 : &tm_k32,
+                              bar + XB_STR_FULL + s, it.w, t);
             }
             if (ok) issued[h] = n + 1;
           }
@@ -417,10 +414,12 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         const int s = 2 * (int)(m & 1) + h;
         if (!W(XB_STR_FULL + s, m >> 1)) return false;
         if (a.kv_len != nullptr && it.len < a.n_kv && (it.dkv || h == 0)) {
-          const int32_t r0 = it.dkv
-                                 ? (it.len - (int32_t)a.q_pos0 - (it.q_tile + t) * tpt) * a.R
-                                 : it.len - win_key0(it.w, t);
-          if (r0 < 128) win_clear_rows(base + kWbOffStream + s * 32768, r0, lane);
+          uint8_t* rows = base + kWbOffStream + s * 32768;
+          if (it.dkv)
+            win_clear_rows(rows, (it.len - (int32_t)a.q_pos0 - (it.q_tile + t) * tpt) * a.R, 128,
+                           lane);
+          else
+            win_clear_keys(rows, it.w, t, lane);
         }
         return true;
       };
@@ -678,13 +677,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       } else {                                // columns: keys
         const int32_t pos = position();
         for (int32_t t = 0; ok && t < nt; ++t) {
-          const int32_t k0 = win_key0(it.w, t);
-          const uint32_t vis =
-              t < it.w.ns
-                  ? range_bits(0, it.w.s_end - k0, c0)
-                  : range_bits(max(pos - win + 1 - k0, 0), min(pos - k0 + 1, 128), c0) |
-                        range_bits(0, min(min(sink - k0, pos - k0 + 1), 128), c0);
-          ok = tile(std::false_type{}, vis);
+          ok = tile(std::false_type{}, win_visible(it.w, 4 * t + wg, pos, sink));   // 32 keys a thread
         }
       }
       if (!ok) break;
@@ -787,8 +780,9 @@ size_t window_attn_bwd_workspace(const WindowArgs& a) {
 }
 
 cudaError_t launch_window_attn_bwd(const CUtensorMap& tm_q, const CUtensorMap& tm_do,
-                                   const CUtensorMap& tm_k, const CUtensorMap& tm_v, WindowArgs a,
-                                   void* ws, cudaStream_t st) {
+                                   const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                   const CUtensorMap& tm_k32, const CUtensorMap& tm_v32,
+                                   WindowArgs a, void* ws, cudaStream_t st) {
   static KernelSetup setup;
   int sms = 0;
   cudaError_t e = kernel_setup(setup, reinterpret_cast<const void*>(window_attn_bwd_kernel), kWbSmemBytes, kWbRegsAtLaunch, &sms);
@@ -819,7 +813,7 @@ cudaError_t launch_window_attn_bwd(const CUtensorMap& tm_q, const CUtensorMap& t
       a, delta, table, pbase, p.counter, pl.chunk, p.nblk);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   window_attn_bwd_kernel<<<(unsigned)min64(p.n_all, sms), kWbThreads, kWbSmemBytes, st>>>(
-      tm_q, tm_do, tm_k, tm_v, p);
+      tm_q, tm_do, tm_k, tm_v, tm_k32, tm_v32, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (pl.n_part > 0) {
     const int32_t n_c = (int32_t)(pl.c_hi - pl.c_lo);

@@ -21,12 +21,14 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // An item: one or two adjacent row tiles (128 / R queries x R heads each) of
-// one (batch, group), and its key tiles: `ns` tiles of sinks [0, s_end) that lie
-// before the window, then tiles of 128 keys from `wlo` on.
+// one (batch, group), and its key tiles: the `nc` chunks of 32 keys that hold the
+// sinks [0, s_end) before the window, then the window's from wlo on, four chunks a
+// tile.  (A tile of its own for a few sinks is a tenth of the work of a
+// 1024-key window.)  Sinks that reach the window make one run from key 0.
 struct WinItem {
   int32_t b, g, i0;          // first query of row tile A
   int32_t q_pos0, W, len;    // len: min(kv_len[b], n_kv)
-  int32_t wlo, s_end, ns, nt;
+  int32_t wlo, s_end, nc, nt;
   int32_t end_a, beg_b;      // last key tile that A sees; first behind the sinks that B sees
   bool rows[2];              // row tile X has a query below n_q and len
   int32_t x0[2], x1[2];      // positions of its first and last such query
@@ -65,26 +67,68 @@ __device__ __forceinline__ void win_item(WinItem& it, const WindowArgs& a, int64
     }
   }
   it.wlo = max(0, tlo - it.W + 1);
+  if (a.sink >= it.wlo) it.wlo = 0;
   it.s_end = (int32_t)min64(a.sink, it.wlo);
-  it.ns = thi < 0 ? 0 : (it.s_end + 127) / 128;
-  it.nt = thi < 0 ? 0 : it.ns + (thi + 1 - it.wlo + 127) / 128;
-  it.end_a = it.rows[0] ? it.ns + (it.x1[0] - it.wlo) / 128 : -1;
-  // (sinks that reach past wlo are visible to B from the first tile on)
-  it.beg_b = it.rows[1] && a.sink <= it.wlo ? it.ns + max(0, it.x0[1] - it.W + 1 - it.wlo) / 128
-                                            : it.ns;
+  it.nc = thi < 0 ? 0 : (it.s_end + 31) / 32;
+  it.nt = thi < 0 ? 0 : (it.nc + (thi + 1 - it.wlo + 31) / 32 + 3) / 4;
+  it.end_a = it.rows[0] ? (it.nc + (it.x1[0] - it.wlo) / 32) / 4 : -1;
+  it.beg_b = it.rows[1] && a.sink <= it.wlo && it.wlo > 0
+                 ? (it.nc + max(0, it.x0[1] - it.W + 1 - it.wlo) / 32) / 4
+                 : 0;
 }
-__device__ __forceinline__ int32_t win_key0(const WinItem& it, int j) {
-  return j < it.ns ? 128 * j : it.wlo + 128 * (j - it.ns);
+// first key of chunk q; the tile of chunks 4 j .. 4 j + 3 is one run of keys unless mixed
+__device__ __forceinline__ int32_t win_chunk(const WinItem& it, int q) {
+  return q < it.nc ? 32 * q : it.wlo + 32 * (q - it.nc);
+}
+__device__ __forceinline__ bool win_mixed(const WinItem& it, int j) {
+  return 4 * j < it.nc && 4 * j + 4 > it.nc;
+}
+// columns lo .. hi - 1 of the 32 from c0 on, as bits
+__device__ __forceinline__ uint32_t range_bits(int32_t lo, int32_t hi, int32_t c0) {
+  lo = max(lo - c0, 0);
+  hi = min(hi - c0, 32);
+  if (lo >= hi) return 0u;
+  return (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
+}
+// of chunk q's 32 keys, those that the query at position t sees, as bits
+__device__ __forceinline__ uint32_t win_visible(const WinItem& it, int q, int32_t t,
+                                                int32_t sink) {
+  const int32_t kc = win_chunk(it, q), hi = t + 1 - kc;
+  return q < it.nc ? range_bits(0, it.s_end - kc, 0)
+                   : range_bits(hi - it.W, hi, 0) | range_bits(0, min(sink - kc, hi), 0);
+}
+// brings key tile j by TMA: two 128 x 64 boxes, or 32 x 64 ones for a mixed tile
+__device__ __forceinline__ void win_load_keys(uint8_t* dst, const CUtensorMap* tm,
+                                              const CUtensorMap* tm32, uint64_t* bar,
+                                              const WinItem& it, int j) {
+  if (!win_mixed(it, j)) {
+    const int32_t k0 = win_chunk(it, 4 * j);
+    tma_load_4d(dst, tm, bar, 0, k0, it.g, it.b);
+    tma_load_4d(dst + 16384, tm, bar, 64, k0, it.g, it.b);
+  } else {
+    for (int i = 0; i < 8; ++i)
+      tma_load_4d(dst + (i >> 2) * 16384 + (i & 3) * 4096, tm32, bar, 64 * (i >> 2),
+                  win_chunk(it, 4 * j + (i & 3)), it.g, it.b);
+  }
 }
 
-// zeroes rows r0 .. 127 of a 128 x 128 bf16 tile (two 64-column panels), by a warp
-__device__ __forceinline__ void win_clear_rows(uint8_t* tile, int32_t r0, int lane) {
+// zeroes rows r0 .. r1 - 1 of a 128 x 128 bf16 tile (two 64-column panels), by a warp
+__device__ __forceinline__ void win_clear_rows(uint8_t* tile, int32_t r0, int32_t r1, int lane) {
   r0 = max(r0, 0);
-  for (int r = r0; r < 128; ++r)
+  for (int r = r0; r < r1; ++r)
     *reinterpret_cast<uint2*>(tile + (lane >> 4) * 16384 + r * 128 + (lane & 15) * 8) =
         make_uint2(0, 0);
   fence_proxy_async_smem();
   __syncwarp();
+}
+// the rows of key tile j at or behind the sequence's end
+__device__ __forceinline__ void win_clear_keys(uint8_t* tile, const WinItem& it, int j,
+                                               int lane) {
+  for (int i = 0; i < 4; ++i) {
+    const int32_t k0 = win_chunk(it, 4 * j + i);
+    if (k0 + 32 > it.len)
+      win_clear_rows(tile, 32 * i + max(it.len - k0, 0), 32 * i + 32, lane);
+  }
 }
 
 }  // namespace msa

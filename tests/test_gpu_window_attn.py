@@ -38,6 +38,11 @@ CASES = [
     (2, 70, 1111, 900, 32, 2, 2000, 0, [905, 1111]),
     (1, 50, 900, 850, 8, 8, 100, 700, None),         # sinks run into the window
     (1, 2500, 2500, 0, 8, 8, 40, 300, None),
+    # sinks and window in one key tile; the sequence ends inside the sinks' 32 keys
+    (1, 900, 900, 0, 4, 1, 70, 45, None),
+    (2, 300, 700, 400, 8, 1, 150, 97, [700, 433]),
+    (1, 5, 40, 10, 4, 1, 1, 3, [13]),
+    (2, 260, 600, 300, 16, 1, 33, 129, [560, 301]),
 ]
 
 
