@@ -179,10 +179,12 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       return true;
     };
     for (uint32_t k = 0; ok; ++k) {
-      const int32_t i = (int32_t)(blockIdx.x + k * gridDim.x);
+      // largest first, the rounds in alternating directions: evens out the CTAs' sums
+      const uint32_t at = (k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+      const int64_t i = (int64_t)k * gridDim.x + at;
       if (k >= 2 && !W(WB_ITEM_EMPTY + (int)(k & 1), (k >> 1) - 1)) break;
       const bool end = i >= n_items;
-      if (!end) win_item(it, a, i, tiles_per_item);
+      if (!end) win_item(it, a, (int32_t)i, tiles_per_item);
       if (lane == 0) {
         *item_slot(k) = it;
         if (end) item_slot(k)->nt = -1;
@@ -520,11 +522,11 @@ cudaError_t launch_window_attn_fwd(const CUtensorMap& tm_q, const CUtensorMap& t
   int sms = 0;
   cudaError_t e = kernel_setup(setup, reinterpret_cast<const void*>(window_attn_fwd_kernel), kWaSmemBytes, kWaRegsAtLaunch, &sms);
   if (e != cudaSuccess) return e;
-  // two row tiles per item overlap their products and softmax; one per item
-  // when that would leave SMs without work
+  // two row tiles per item share the key tiles' loads (8192 tokens, 64 heads: 274 us, one
+  // per item 373); one per item when all of them run at once (1024 tokens, 16 heads: 16.4
+  // us, two per item 18.5; twice the tokens: 26.6 and 20.5)
   const int64_t tiles = (a.n_q * a.R + 127) / 128;
-  int32_t per = 2;
-  if (a.batch * a.G * ((tiles + 1) / 2) < sms) per = 1;
+  const int32_t per = a.batch * a.G * tiles <= sms ? 1 : 2;
   const int64_t items = a.batch * a.G * ((tiles + per - 1) / per);
   if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
   window_attn_fwd_kernel<<<(unsigned)min64(items, sms), kWaThreads, kWaSmemBytes, st>>>(

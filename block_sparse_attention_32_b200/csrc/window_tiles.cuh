@@ -42,15 +42,15 @@ __device__ __forceinline__ int32_t win_len(const WindowArgs& a, int32_t b) {
   return max(0, min(v, n));
 }
 
-// items in descending query order: with no window the longest rows go first
-__device__ __forceinline__ void win_item(WinItem& it, const WindowArgs& a, int64_t i,
+// items in descending query order over all (batch, group): with no window the
+// longest rows go first
+__device__ __forceinline__ void win_item(WinItem& it, const WindowArgs& a, int32_t i,
                                          int32_t per) {
-  const int32_t tpt = 128 / a.R;
-  const int64_t n_it = (a.n_q + (int64_t)tpt * per - 1) / ((int64_t)tpt * per);
-  const int64_t bg = i / n_it;
-  it.b = (int32_t)(bg / a.G);
-  it.g = (int32_t)(bg - (int64_t)it.b * a.G);
-  it.i0 = (int32_t)(n_it - 1 - (i - bg * n_it)) * tpt * per;
+  const int32_t step = 128 / a.R * per, n_it = ((int32_t)a.n_q + step - 1) / step;
+  const int32_t tpt = 128 / a.R, n_bg = (int32_t)a.batch * a.G, r = i / n_bg, bg = i - r * n_bg;
+  it.b = bg / a.G;
+  it.g = bg - it.b * a.G;
+  it.i0 = (n_it - 1 - r) * step;
   it.q_pos0 = (int32_t)a.q_pos0;
   it.W = a.window > 0 ? (int32_t)min64(a.window, int64_t(1) << 30) : 1 << 30;
   it.len = win_len(a, it.b);
