@@ -54,16 +54,28 @@ __device__ __forceinline__ void unpack8(const uint4& u, Row8& x) {
     x.v[3] = pack_f32x2(u.w << 16, u.w & kHi);
   }
 }
+// the same as plain floats: partners at j and j + 4
 template <bool kInter>
-__device__ __forceinline__ uint4 pack8(const Row8& x) {
-  float f[8];
+__device__ __forceinline__ void floats8(const uint4& u, float (&x)[8]) {
+  Row8 r;
+  unpack8<kInter>(u, r);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) unpack_f32x2(x.v[i], f[2 * i], f[2 * i + 1]);
+  for (int j = 0; j < 4; ++j) unpack_f32x2(r.v[j], x[2 * j], x[2 * j + 1]);
+}
+template <bool kInter>
+__device__ __forceinline__ uint4 words8(const float (&f)[8]) {
   if (kInter)
     return make_uint4(pack_bf16x2(f[0], f[4]), pack_bf16x2(f[1], f[5]), pack_bf16x2(f[2], f[6]),
                       pack_bf16x2(f[3], f[7]));
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                     pack_bf16x2(f[6], f[7]));
+}
+template <bool kInter>
+__device__ __forceinline__ uint4 pack8(const Row8& x) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack_f32x2(x.v[i], f[2 * i], f[2 * i + 1]);
+  return words8<kInter>(f);
 }
 // two runs of four fp32 values (o0.., o1..)
 template <bool kInter>
@@ -188,7 +200,8 @@ __device__ __forceinline__ int64_t token_pos(const NormRopeArgs& a, int64_t bt, 
   return p;
 }
 
-constexpr int kNrThreads = 256;
+constexpr int kNrThreads = 128;    // forward
+constexpr int kNrBwdThreads = 256;
 constexpr int kNrHeads = 8;        // heads of a token per item; all loaded before the first is used
 
 template <int kD, bool kInter, bool kPaged>
@@ -240,22 +253,40 @@ __global__ void __launch_bounds__(kNrThreads)
     }
   }
   Angles ang;
-  Row8 w;
+  Row8 wp;
   const bool norm = !kPaged || kind < 2;
   load_angles(a.table + (live ? pos : 0) * a.rot, a.rot, lp, live && norm, ang);
-  load_weights<kInter>(norm ? a.w[kPaged ? min(kind, 1) : kind] : nullptr, lp, w);
+  load_weights<kInter>(norm ? a.w[kPaged ? min(kind, 1) : kind] : nullptr, lp, wp);
+  // plain fp32 from here on: with packed pairs as in the backward the compiler needs more
+  // registers and moves (32768 tokens, 40 heads: 131 us, 113 like this)
+  float c[4], sn[4], w[8];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    unpack_f32x2(ang.c[j], c[2 * j], c[2 * j + 1]);
+    unpack_f32x2(ang.s[j], sn[2 * j], sn[2 * j + 1]);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) unpack_f32x2(wp.v[j], w[2 * j], w[2 * j + 1]);
 #pragma unroll
   for (int u = 0; u < kNrHeads; ++u) {
     if (u >= a.hc) break;                           // the same for every lane
-    Row8 x;
-    unpack8<kInter>(v[u], x);
-    const float ss = row_sum<kLanes>(dot8(x, x));
-    const uint64_t r = dup_f32x2(rsqrtf(ss * (1.f / kD) + a.eps));
+    float x[8];
+    floats8<kInter>(v[u], x);
+    float ss = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x.v[j] = mul_f32x2(mul_f32x2(x.v[j], r), w.v[j]);
-    rotate8<1>(x, ang);
+    for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
+    ss = row_sum<kLanes>(ss);
+    const float r = rsqrtf(ss * (1.f / kD) + a.eps);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float p = x[j], q = x[j + 4];
+      x[j] = p * c[j] - q * sn[j];
+      x[j + 4] = q * c[j] + p * sn[j];
+    }
     if (live && h0 + u < h1)
-      store_row<kInter>(dst + u * a.ds_h[kind], lp, norm ? pack8<kInter>(x) : v[u]);
+      store_row<kInter>(dst + u * a.ds_h[kind], lp, norm ? words8<kInter>(x) : v[u]);
   }
 }
 
@@ -290,9 +321,9 @@ __device__ __forceinline__ void unpack_dy(const uint4 (&v)[2], Row8& y) {
 constexpr int kNrBwdUnroll = 4;    // rows in flight per lane
 
 template <int kD, bool kInter, bool kF32>
-__global__ void __launch_bounds__(kNrThreads, 2)
+__global__ void __launch_bounds__(kNrBwdThreads, 2)
     norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdArgs p) {
-  constexpr int kLanes = kD / 8, kGroups = kNrThreads / kLanes, kU = kNrBwdUnroll;
+  constexpr int kLanes = kD / 8, kGroups = kNrBwdThreads / kLanes, kU = kNrBwdUnroll;
   const NormRopeArgs& a = p.f;
   __shared__ float red[kGroups][kD + 4];
   const int ln = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
@@ -460,17 +491,17 @@ template <int kD>
 static void pick_bwd(const NormRopeBwdArgs& p, bool inter, bool f32, unsigned grid,
                      cudaStream_t st) {
   if (f32) {
-    if (inter) norm_rope_bwd_kernel<kD, true, true><<<grid, kNrThreads, 0, st>>>(p);
-    else norm_rope_bwd_kernel<kD, false, true><<<grid, kNrThreads, 0, st>>>(p);
+    if (inter) norm_rope_bwd_kernel<kD, true, true><<<grid, kNrBwdThreads, 0, st>>>(p);
+    else norm_rope_bwd_kernel<kD, false, true><<<grid, kNrBwdThreads, 0, st>>>(p);
   } else {
-    if (inter) norm_rope_bwd_kernel<kD, true, false><<<grid, kNrThreads, 0, st>>>(p);
-    else norm_rope_bwd_kernel<kD, false, false><<<grid, kNrThreads, 0, st>>>(p);
+    if (inter) norm_rope_bwd_kernel<kD, true, false><<<grid, kNrBwdThreads, 0, st>>>(p);
+    else norm_rope_bwd_kernel<kD, false, false><<<grid, kNrBwdThreads, 0, st>>>(p);
   }
 }
 
 cudaError_t launch_norm_rope_bwd(NormRopeBwdArgs p, int32_t d, bool inter, bool f32, float* dw_q,
                                  float* dw_k, cudaStream_t st) {
-  const int groups = kNrThreads / (d / 8);
+  const int groups = kNrBwdThreads / (d / 8);
   split_heads(p.f, 2, 8);
   if (p.f.n_items < (int64_t)kNrBwdBlocks * groups * 4) split_heads(p.f, 2, 2);
   if (p.f.n_items > 0x7FFFFF00) return cudaErrorInvalidValue;
