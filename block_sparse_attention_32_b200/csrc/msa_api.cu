@@ -674,6 +674,24 @@ msa_status check_paged(const msa_paged_kv* c) {
   return MSA_OK;
 }
 
+// every (batch, token, head) row has a place of its own
+bool rows_apart(const msa_tensor& t, int64_t batch, int64_t tok, int64_t heads) {
+  return (t.s_batch > 0 || batch == 1) && (t.s_tok > 0 || tok == 1) &&
+         (t.s_head > 0 || heads == 1);
+}
+// outputs of the norms: checked like inputs, and no two rows in one place
+msa_status check_norm_out(const msa_tensor& t, const msa_norm_rope_dims* d, int64_t heads) {
+  const msa_status s = check_tensor(t);
+  if (s != MSA_OK) return s;
+  return rows_apart(t, d->batch, d->n_tok, heads) ? MSA_OK : MSA_ERR_INVALID_ARG;
+}
+// tensors read through TMA maps, which have no stride of 0
+msa_status check_mapped(const msa_tensor& t, int64_t batch, int64_t tok, int64_t heads) {
+  const msa_status s = check_tensor(t);
+  if (s != MSA_OK) return s;
+  return rows_apart(t, batch, tok, heads) ? MSA_OK : MSA_ERR_UNSUPPORTED;
+}
+
 // check_tensor for strides in elements of `bytes` bytes
 msa_status check_rows(const msa_tensor& t, int bytes) {
   const msa_status s = check_tensor(t);
@@ -790,10 +808,12 @@ msa_status msa_qk_norm_rope(const msa_norm_rope_dims* d, msa_tensor q, msa_tenso
                             msa_tensor k_out, int32_t* dev_err, void* stream) {
   msa_status s = check_norm_rope(d, w_q, w_k, table, n_pos, positions);
   if (s != MSA_OK) return s;
-  for (const msa_tensor* t : {&q, &q_out})
-    if (d->h_q > 0 && (s = check_tensor(*t)) != MSA_OK) return s;
-  for (const msa_tensor* t : {&k, &k_out})
-    if (d->h_k > 0 && (s = check_tensor(*t)) != MSA_OK) return s;
+  if (d->h_q > 0 && ((s = check_tensor(q)) != MSA_OK ||
+                     (s = check_norm_out(q_out, d, d->h_q)) != MSA_OK))
+    return s;
+  if (d->h_k > 0 && ((s = check_tensor(k)) != MSA_OK ||
+                     (s = check_norm_out(k_out, d, d->h_k)) != MSA_OK))
+    return s;
   msa::NormRopeArgs a = norm_rope_args(d, w_q, w_k, table, n_pos, positions, dev_err);
   set_src(a, 0, q);
   set_src(a, 1, k);
@@ -813,8 +833,9 @@ msa_status msa_qk_norm_rope_paged(const msa_norm_rope_dims* d, msa_tensor q, msa
   if (d->d != MSA_HEAD_DIM) return MSA_ERR_UNSUPPORTED;
   if ((s = check_paged(cache)) != MSA_OK) return s;
   if (d->h_k != cache->h_kv) return MSA_ERR_INVALID_ARG;
-  for (const msa_tensor* t : {&q, &q_out})
-    if (d->h_q > 0 && (s = check_tensor(*t)) != MSA_OK) return s;
+  if (d->h_q > 0 && ((s = check_tensor(q)) != MSA_OK ||
+                     (s = check_norm_out(q_out, d, d->h_q)) != MSA_OK))
+    return s;
   if ((s = check_tensor(k)) != MSA_OK) return s;
   if ((s = check_tensor(v)) != MSA_OK) return s;
   msa::NormRopeArgs a = norm_rope_args(d, w_q, w_k, table, n_pos, positions, dev_err);
@@ -847,10 +868,12 @@ msa_status msa_qk_norm_rope_bwd(const msa_norm_rope_dims* d, msa_tensor q, msa_t
   msa_status s = check_norm_rope(d, w_q, w_k, table, n_pos, positions);
   if (s != MSA_OK) return s;
   if (dy_fp32 != 0 && dy_fp32 != 1) return MSA_ERR_INVALID_ARG;
-  for (const msa_tensor* t : {&q, &dx_q})
-    if (d->h_q > 0 && (s = check_tensor(*t)) != MSA_OK) return s;
-  for (const msa_tensor* t : {&k, &dx_k})
-    if (d->h_k > 0 && (s = check_tensor(*t)) != MSA_OK) return s;
+  if (d->h_q > 0 && ((s = check_tensor(q)) != MSA_OK ||
+                     (s = check_norm_out(dx_q, d, d->h_q)) != MSA_OK))
+    return s;
+  if (d->h_k > 0 && ((s = check_tensor(k)) != MSA_OK ||
+                     (s = check_norm_out(dx_k, d, d->h_k)) != MSA_OK))
+    return s;
   if (d->h_q > 0 && (s = check_rows(d_q, dy_fp32 ? 4 : 2)) != MSA_OK) return s;
   if (d->h_k > 0 && (s = check_rows(d_k, dy_fp32 ? 4 : 2)) != MSA_OK) return s;
   if (ws == nullptr) return MSA_ERR_INVALID_ARG;
@@ -933,8 +956,9 @@ msa_status msa_window_attn_fwd(const msa_dims* d, int64_t window, int64_t n_sink
                                void* out_rest, float* lse, int32_t* dev_err, void* stream) {
   msa_status s = check_window(d, window, n_sink, kv_len);
   if (s != MSA_OK) return s;
-  for (const msa_tensor* t : {&q, &k, &v})
-    if ((s = check_tensor(*t)) != MSA_OK) return s;
+  if ((s = check_mapped(q, d->batch, d->n_q, d->h_q)) != MSA_OK) return s;
+  for (const msa_tensor* t : {&k, &v})
+    if ((s = check_mapped(*t, d->batch, d->n_kv, d->h_kv)) != MSA_OK) return s;
   if (out == nullptr || lse == nullptr) return MSA_ERR_INVALID_ARG;
   if (!aligned32(out) || !aligned16(out_rest) || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return MSA_ERR_ALIGNMENT;
@@ -965,8 +989,11 @@ msa_status msa_window_attn_bwd(const msa_dims* d, int64_t window, int64_t n_sink
                                void* stream) {
   msa_status s = check_window(d, window, n_sink, kv_len);
   if (s != MSA_OK) return s;
-  for (const msa_tensor* t : {&q, &k, &v, &o, &d_o})
-    if ((s = check_tensor(*t)) != MSA_OK) return s;
+  for (const msa_tensor* t : {&q, &d_o})
+    if ((s = check_mapped(*t, d->batch, d->n_q, d->h_q)) != MSA_OK) return s;
+  for (const msa_tensor* t : {&k, &v})
+    if ((s = check_mapped(*t, d->batch, d->n_kv, d->h_kv)) != MSA_OK) return s;
+  if ((s = check_tensor(o)) != MSA_OK) return s;
   if (lse == nullptr || dq == nullptr || dk == nullptr || dv == nullptr || ws == nullptr)
     return MSA_ERR_INVALID_ARG;
   if (!aligned32(dq) || !aligned32(dk) || !aligned32(dv) || !aligned32(ws) || !aligned16(o_rest) ||

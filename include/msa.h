@@ -428,7 +428,8 @@ typedef struct {
  *             positions pos0 + n_tok <= n_pos is required.
  *   q_out     [B, n_tok, h_q, d], k_out: the same for h_k; any strides, so k_out
  *             can be the attention's [B, h_k, n, d].  An output may be its input
- *             itself (same pointer and strides), not overlap it otherwise. */
+ *             itself (same pointer and strides), not overlap it otherwise.  An
+ *             input's stride may be 0 (a broadcast dimension), an output's not. */
 MSA_API msa_status msa_qk_norm_rope(const msa_norm_rope_dims* dims, msa_tensor q, msa_tensor k,
                                     const float* w_q, const float* w_k, const float* table,
                                     int64_t n_pos, const int64_t* positions, msa_tensor q_out,
@@ -522,7 +523,8 @@ MSA_API msa_status msa_paged_decode_attn(const msa_dims* dims, int64_t window, i
  *          each bf16 of out, so that the fp32 with the bits (out << 16) + (rest << 8)
  *          is o to 2^-17.  The backward's D = dO.o takes it: from the rounded out
  *          alone D is off by up to 2^-9 sum |dO o|, which reaches dq and dk.
- * K and V must be finite at the keys below kv_len. */
+ * K and V must be finite at the keys below kv_len.  A stride of 0 over a dimension
+ * of extent > 1 (q, k, v; d_o in the backward) is MSA_ERR_UNSUPPORTED. */
 MSA_API msa_status msa_window_attn_fwd(const msa_dims* dims, int64_t window, int64_t n_sink,
                                        msa_tensor q, msa_tensor k, msa_tensor v,
                                        const int32_t* kv_len, void* out, void* out_rest,

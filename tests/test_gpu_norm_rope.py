@@ -131,6 +131,24 @@ def test_views_of_a_fused_projection_in_place_and_missing_parts():
     assert none is None and torch.equal(k_out.transpose(1, 2), k)
 
 
+def test_broadcast_inputs():
+    """One row for all tokens and heads (strides of 0), also as upstream gradient."""
+    row, g = _rn(1, 1, 1, 1, 128), _rn(2, 1, 1, 1, 128)
+    x, dy = row.expand(2, 5, 3, 128), g.expand(2, 5, 3, 128)
+    table = pipeline.rope_table(5, 32)
+    plan = pipeline.NormRope(table, _w(3, 128))
+    out, _ = pipeline.norm_rope(plan, x, None)
+    gr = pipeline.NormRopeGrads.allocate(x, None)
+    dx, _, dw, _ = pipeline.norm_rope_backward(plan, x, None, dy, None, gr)
+    pos = torch.arange(5, device="cuda")[None].expand(2, -1)
+    cos, sin = ref.angles(table, pos)
+    want, bound = ref.norm_rope(x, plan.w_q, cos, sin, False, 1e-6)
+    ref.close("y", out, want, bound)
+    ex, bx, ew, bw = ref.norm_rope_bwd(x, plan.w_q, dy, cos, sin, False, 1e-6, pos >= 0)
+    ref.close("dx", dx, ex, bx)
+    ref.close("dw", dw, ew, bw, fro=False)
+
+
 def test_zero_rows_and_eps_zero():
     """A zero row stays zero; with eps = 0 absent rows add nothing to dw."""
     q = _rn(1, 1, 6, 3, 64)

@@ -210,6 +210,44 @@ def test_rows_far_above_the_first_maximum():
     ref.close_lse(lse[0], l)
 
 
+def test_more_than_31_bits_of_elements():
+    """2^31 elements of q and out: rows at both ends against the definition, forward and
+    backward."""
+    n, H, W = 262144 + 200, 64, 30
+    q = torch.empty((1, n, H, 128), dtype=BF, device="cuda").normal_()
+    k, v = _rn(2, 1, 4, n, 128), _rn(3, 1, 4, n, 128)
+    buf = pipeline.WindowBuffers.allocate(pipeline.window_dims(1, n, n, 0, H, 4), W, 2,
+                                          backward=True)
+    out, lse = pipeline.window_forward(buf, q, k, v)
+    d_o = q
+    dq, dk, dv = pipeline.window_backward(buf, q, k, v, d_o)
+    assert int(buf.dev_err[0]) == 0
+    for i0 in (0, 131072, n - 40):
+        # 40 queries, their window's keys and the two sinks
+        lo = max(2, i0 - W + 1)
+        keys = torch.cat([torch.arange(2), torch.arange(lo, i0 + 40)]).cuda()
+        t = torch.arange(i0, i0 + 40, device="cuda")[:, None]
+        see = (keys[None] <= t) & ((t - keys[None] < W) | (keys[None] < 2))
+        sq, sk, sv = q[0, i0:i0 + 40], k[0][:, keys], v[0][:, keys]
+        o, l, bound, aux = ref.attention(sq, sk, sv, see, 1 / math.sqrt(128))
+        ref.close("o", out[0, i0:i0 + 40], o, bound)
+        ref.close_lse(lse[0, i0:i0 + 40], l)
+        (eq, bq), _, _ = ref.attention_grads(o, aux, d_o[0, i0:i0 + 40], see, 1 / math.sqrt(128), 4)
+        ref.close("dq", dq[0, i0:i0 + 40], eq, bq)
+    # the last keys are seen by the last queries alone
+    i0 = n - 60
+    keys = torch.arange(i0 - W + 1, n, device="cuda")
+    t = torch.arange(i0, n, device="cuda")[:, None]
+    see = (keys[None] <= t) & (t - keys[None] < W)
+    sinks = torch.arange(2, device="cuda")
+    see = torch.cat([torch.ones((60, 2), dtype=torch.bool, device="cuda"), see], 1)
+    keys = torch.cat([sinks, keys])
+    o, l, bound, aux = ref.attention(q[0, i0:], k[0][:, keys], v[0][:, keys], see, 1 / math.sqrt(128))
+    _, (ek, bk), (ev, bv) = ref.attention_grads(o, aux, d_o[0, i0:], see, 1 / math.sqrt(128), 4)
+    ref.close("dk", dk[0, :, -31:], ek[:, -31:], bk[:, -31:])
+    ref.close("dv", dv[0, :, -31:], ev[:, -31:], bv[:, -31:])
+
+
 def test_bad_length_is_reported_and_clamped():
     case = (2, 40, 100, 60, 4, 1, 0, 0, [100, 0])
     q, k, v, d_o, _ = _inputs(case, nan=False)

@@ -134,7 +134,24 @@ def test_paged_decode_refuses_bad_caches(lib, want, kw):
     assert _decode(lib, cache=_cache(**kw)) == want
 
 
+def test_broadcast_strides(lib):
+    """Inputs of the norms may be broadcast, outputs not; tensors read by TMA not."""
+    flat = capi.Tensor(0x100000, 1 << 20, 0, 128)
+    assert _norm(lib, qo=flat) == INVALID and _norm(lib, ko=capi.Tensor(0x100000, 0, 0, 128)) == INVALID
+    assert _norm(lib, batch=2, qo=GOOD) == INVALID
+    assert _norm(lib, batch=2, q=flat, qo=flat) == INVALID
+    d = capi.make_dims(2, 100, 300, 200, 8, 2, 128)
+    good, shared = capi.Tensor(0x100000, 1 << 20, 1024, 128), capi.Tensor(0x100000, 0, 1024, 128)
+    for q, k, v in ((shared, good, good), (good, shared, good), (good, good, shared)):
+        assert lib.msa_window_attn_fwd(ctypes.byref(d), 0, 0, q, k, v, None, P(0x100000), None,
+                                       P(0x2000), None, None) == UNSUPPORTED
+    assert lib.msa_window_attn_bwd(ctypes.byref(d), 0, 0, good, good, good, good, None, shared,
+                                   P(0x2000), None, P(0x100000), P(0x100000), P(0x100000),
+                                   P(0x5000), 1 << 40, None, None) == UNSUPPORTED
+
+
 def test_window_statuses(lib):
+    GOOD = capi.Tensor(0x100000, 1 << 20, 256, 128)
     d = capi.make_dims(2, 100, 300, 200, 8, 2, 128)
     f, b = lib.msa_window_attn_fwd, lib.msa_window_attn_bwd
 
