@@ -293,46 +293,153 @@ __global__ void __launch_bounds__(kNrThreads)
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-template <bool kInter, bool kF32>
-__device__ __forceinline__ void load_dy(const void* p, int64_t off, const LanePos& l,
-                                        uint4 (&v)[2]) {
-  if (kF32) {
-    const float* y = reinterpret_cast<const float*>(p) + off;
-    v[0] = *reinterpret_cast<const uint4*>(y + l.o0);
-    v[1] = *reinterpret_cast<const uint4*>(y + l.o1);
+// Backward lanes hold 16 features, two runs of 8 (D / 16 lanes a row): the sums'
+// shuffles, the square root and the addresses of a row, half of the forward's kind of
+// work, are shared by twice the features.  v[j] and v[j + 4] hold partners.
+struct Row16 {
+  uint64_t v[8];
+};
+template <bool kInter>
+__device__ __forceinline__ LanePos lane_pos16(int ln, int rot) {
+  LanePos p;
+  p.ang = 8 * ln;
+  if (kInter) {
+    p.turns = 16 * ln < rot;
+    p.o0 = 16 * ln;
+    p.o1 = 16 * ln + 8;
   } else {
-    v[0] = load_row<kInter>(reinterpret_cast<const __nv_bfloat16*>(p) + off, l);
+    const int half = rot >> 1;          // a multiple of 8
+    p.turns = 8 * ln < half;
+    p.o0 = p.turns ? 8 * ln : 16 * ln;
+    p.o1 = p.turns ? half + 8 * ln : 16 * ln + 8;
+  }
+  return p;
+}
+template <bool kInter>
+__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, Row16& x) {
+  Row8 r0, r1;
+  unpack8<kInter>(a, r0);               // runs of 8: (0, 1 | 2, 3) partners, or plain pairs
+  unpack8<kInter>(b, r1);
+  if (kInter) {
+    x.v[0] = r0.v[0]; x.v[1] = r0.v[1]; x.v[2] = r1.v[0]; x.v[3] = r1.v[1];
+    x.v[4] = r0.v[2]; x.v[5] = r0.v[3]; x.v[6] = r1.v[2]; x.v[7] = r1.v[3];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x.v[j] = r0.v[j];
+      x.v[4 + j] = r1.v[j];
+    }
   }
 }
-template <bool kInter, bool kF32>
-__device__ __forceinline__ void unpack_dy(const uint4 (&v)[2], Row8& y) {
-  if (kF32)
-    arrange8<kInter>(make_float4(u2f(v[0].x), u2f(v[0].y), u2f(v[0].z), u2f(v[0].w)),
-                     make_float4(u2f(v[1].x), u2f(v[1].y), u2f(v[1].z), u2f(v[1].w)), y);
-  else
-    unpack8<kInter>(v[0], y);
+template <bool kInter>
+__device__ __forceinline__ void pack16(const Row16& x, uint4& a, uint4& b) {
+  Row8 r0, r1;
+  if (kInter) {
+    r0.v[0] = x.v[0]; r0.v[1] = x.v[1]; r1.v[0] = x.v[2]; r1.v[1] = x.v[3];
+    r0.v[2] = x.v[4]; r0.v[3] = x.v[5]; r1.v[2] = x.v[6]; r1.v[3] = x.v[7];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      r0.v[j] = x.v[j];
+      r1.v[j] = x.v[4 + j];
+    }
+  }
+  a = pack8<kInter>(r0);
+  b = pack8<kInter>(r1);
+}
+// two runs of eight fp32 values
+template <bool kInter>
+__device__ __forceinline__ void arrange16(const uint4 (&u)[4], Row16& x) {
+  Row8 r0, r1;
+  auto f = [](const uint4& q) { return make_float4(u2f(q.x), u2f(q.y), u2f(q.z), u2f(q.w)); };
+  arrange8<kInter>(f(u[0]), f(u[1]), r0);
+  arrange8<kInter>(f(u[2]), f(u[3]), r1);
+  if (kInter) {
+    x.v[0] = r0.v[0]; x.v[1] = r0.v[1]; x.v[2] = r1.v[0]; x.v[3] = r1.v[1];
+    x.v[4] = r0.v[2]; x.v[5] = r0.v[3]; x.v[6] = r1.v[2]; x.v[7] = r1.v[3];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x.v[j] = r0.v[j];
+      x.v[4 + j] = r1.v[j];
+    }
+  }
+}
+// feature of element e (0, 1) of v[j]
+template <bool kInter>
+__device__ __forceinline__ int feature16(const LanePos& l, int j, int e) {
+  if (!kInter) return (j < 4 ? l.o0 : l.o1) + 2 * (j & 3) + e;
+  const int i = 2 * (j & 3) + e;        // pair of the lane
+  return l.o0 + 2 * i + (j >> 2);
+}
+
+template <bool kF32>
+struct Grad16 {                         // a lane's upstream gradient as loaded
+  uint4 u[kF32 ? 4 : 2];
+};
+template <bool kF32>
+__device__ __forceinline__ void load_dy(const void* p, int64_t off, const LanePos& l,
+                                        Grad16<kF32>& v) {
+  if (kF32) {
+    const float* y = reinterpret_cast<const float*>(p) + off;
+    v.u[0] = *reinterpret_cast<const uint4*>(y + l.o0);
+    v.u[1] = *reinterpret_cast<const uint4*>(y + l.o0 + 4);
+    v.u[kF32 ? 2 : 0] = *reinterpret_cast<const uint4*>(y + l.o1);
+    v.u[kF32 ? 3 : 1] = *reinterpret_cast<const uint4*>(y + l.o1 + 4);
+  } else {
+    const __nv_bfloat16* y = reinterpret_cast<const __nv_bfloat16*>(p) + off;
+    v.u[0] = *reinterpret_cast<const uint4*>(y + l.o0);
+    v.u[1] = *reinterpret_cast<const uint4*>(y + l.o1);
+  }
+}
+__device__ __forceinline__ float dot16(const Row16& a, const Row16& b) {
+  uint64_t s0 = mul_f32x2(a.v[0], b.v[0]), s1 = mul_f32x2(a.v[1], b.v[1]);
+#pragma unroll
+  for (int j = 2; j < 8; j += 2) {
+    s0 = fma_f32x2(a.v[j], b.v[j], s0);
+    s1 = fma_f32x2(a.v[j + 1], b.v[j + 1], s1);
+  }
+  return sum_f32x2(add_f32x2(s0, s1));
 }
 
 // Persistent blocks over the items, all of the queries' before the keys': the
-// lanes of a row keep their 8 features' weight-gradient sums in fp32 registers
+// lanes of a row keep their 16 features' weight-gradient sums in fp32 registers
 // over all the rows they meet, then the block's rows are added in a fixed order
 // and leave as one partial row; a second kernel adds the blocks in a fixed
 // order.  No atomics: the same bits every run.
-constexpr int kNrBwdUnroll = 4;    // rows in flight per lane
-
 template <int kD, bool kInter, bool kF32>
 __global__ void __launch_bounds__(kNrBwdThreads, 2)
     norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdArgs p) {
-  constexpr int kLanes = kD / 8, kGroups = kNrBwdThreads / kLanes, kU = kNrBwdUnroll;
+  constexpr int kLanes = kD / 16, kGroups = kNrBwdThreads / kLanes, kU = kF32 ? 1 : 2;  // rows
   const NormRopeArgs& a = p.f;
-  __shared__ float red[kGroups][kD + 4];
+  __shared__ float red[kGroups][kD + 4];            // the queries' sums, then the keys'
+  grid_launch_dependents();
   const int ln = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-  const LanePos lp = lane_pos<kInter>(ln, a.rot);
-  Row8 dwq, g, w;
+  const LanePos lp = lane_pos16<kInter>(ln, a.rot);
+  Row16 g, w;
+  auto weights = [&](const float* wp) {
+    uint4 u[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) dwq.v[j] = g.v[j] = 0ull;
+    for (int j = 0; j < 4; ++j) {
+      u[j] = make_uint4(0x3f800000u, 0x3f800000u, 0x3f800000u, 0x3f800000u);
+      if (wp != nullptr)
+        u[j] = __ldg(reinterpret_cast<const uint4*>(wp + (j < 2 ? lp.o0 : lp.o1) + 4 * (j & 1)));
+    }
+    arrange16<kInter>(u, w);
+  };
+  auto put = [&](const Row16& x) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float t[2];
+      unpack_f32x2(x.v[j], t[0], t[1]);
+      red[grp][feature16<kInter>(lp, j, 0)] = t[0];
+      red[grp][feature16<kInter>(lp, j, 1)] = t[1];
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < 8; ++j) g.v[j] = 0ull;
   int cur = 0;                                      // kind that g belongs to
-  load_weights<kInter>(a.w[0], lp, w);
+  weights(a.w[0]);
   const uint32_t n_items = (uint32_t)a.n_items;
   const uint32_t nq = (uint32_t)(a.batch * a.n_tok) * a.chunks[0];
   const uint32_t step = gridDim.x * kGroups;
@@ -349,72 +456,104 @@ __global__ void __launch_bounds__(kNrBwdThreads, 2)
     const uint32_t b = bt / (uint32_t)a.n_tok, i = bt - b * (uint32_t)a.n_tok;
     if (in && kind != cur) {
       cur = kind;
+      put(g);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        dwq.v[j] = g.v[j];
-        g.v[j] = 0ull;
-      }
-      load_weights<kInter>(a.w[1], lp, w);
+      for (int j = 0; j < 8; ++j) g.v[j] = 0ull;
+      weights(a.w[1]);
     }
     const int64_t pos = in ? token_pos(a, bt, i) : -1;
     const bool live = pos >= 0;
-    const int h0 = ch * a.hc, h1 = min(h0 + a.hc, a.heads[kind]);
-    const __nv_bfloat16* src = a.src[kind] + b * a.ss_b[kind] + i * a.ss_t[kind];
-    __nv_bfloat16* dst = a.dst[kind] + b * a.ds_b[kind] + i * a.ds_t[kind];
-    const int64_t yo = b * p.ys_b[kind] + i * p.ys_t[kind];
-    Angles ang;
-    load_angles(a.table + (live ? pos : 0) * a.rot, a.rot, lp, live, ang);
+    const int h0 = ch * a.hc, n_h = live ? min(a.hc, a.heads[kind] - h0) : 0;
+    const __nv_bfloat16* src =
+        a.src[kind] + b * a.ss_b[kind] + i * a.ss_t[kind] + h0 * a.ss_h[kind];
+    __nv_bfloat16* dst = a.dst[kind] + b * a.ds_b[kind] + i * a.ds_t[kind] + h0 * a.ds_h[kind];
+    const int64_t yo = b * p.ys_b[kind] + i * p.ys_t[kind] + h0 * p.ys_h[kind];
+    uint64_t c[4], sn[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      c[j] = dup_f32x2(1.f);
+      sn[j] = 0ull;
+    }
+    if (live && lp.turns) {
+      const float* row = a.table + pos * a.rot + lp.ang;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const ulonglong2 u = __ldg(reinterpret_cast<const ulonglong2*>(row) + j);
+        const ulonglong2 v = __ldg(reinterpret_cast<const ulonglong2*>(row + (a.rot >> 1)) + j);
+        c[2 * j] = u.x; c[2 * j + 1] = u.y;
+        sn[2 * j] = v.x; sn[2 * j + 1] = v.y;
+      }
+    }
     for (int hb = 0; hb < a.hc; hb += kU) {
-      uint4 xv[kU], yv[kU][2];
+      uint4 xv[kU][2];
+      Grad16<kF32> yv[kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int h = h0 + hb + u;
-        xv[u] = yv[u][0] = yv[u][1] = make_uint4(0, 0, 0, 0);
-        if (live && h < h1) {
-          xv[u] = load_row<kInter>(src + h * a.ss_h[kind], lp);
-          load_dy<kInter, kF32>(p.dy[kind], yo + h * p.ys_h[kind], lp, yv[u]);
+        xv[u][0] = xv[u][1] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < (kF32 ? 4 : 2); ++j) yv[u].u[j] = make_uint4(0, 0, 0, 0);
+        if (hb + u < n_h) {
+          const __nv_bfloat16* x = src + (hb + u) * a.ss_h[kind];
+          xv[u][0] = *reinterpret_cast<const uint4*>(x + lp.o0);
+          xv[u][1] = *reinterpret_cast<const uint4*>(x + lp.o1);
+          load_dy<kF32>(p.dy[kind], yo + (hb + u) * p.ys_h[kind], lp, yv[u]);
         }
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int h = h0 + hb + u;
-        if (hb + u >= a.hc) break;                  // the same for every lane
-        Row8 x, y, yw;
-        unpack8<kInter>(xv[u], x);
-        unpack_dy<kInter, kF32>(yv[u], y);
-        rotate8<-1>(y, ang);
+        Row16 x, y;
+        unpack16<kInter>(xv[u][0], xv[u][1], x);
+        if (kF32) {
+          const uint4 q[4] = {yv[u].u[0], yv[u].u[1], yv[u].u[kF32 ? 2 : 0], yv[u].u[kF32 ? 3 : 1]};
+          arrange16<kInter>(q, y);
+        } else {
+          unpack16<kInter>(yv[u].u[0], yv[u].u[1], y);
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) yw.v[j] = mul_f32x2(y.v[j], w.v[j]);
-        const float ss = row_sum<kLanes>(dot8(x, x)), sy = row_sum<kLanes>(dot8(x, yw));
+        for (int j = 0; j < 4; ++j) {               // turned back
+          const uint64_t q = y.v[j], r = y.v[j + 4];
+          y.v[j] = fma_f32x2(r, sn[j], mul_f32x2(q, c[j]));
+          y.v[j + 4] = fma_f32x2(q, neg_f32x2(sn[j]), mul_f32x2(r, c[j]));
+        }
+        float ss = dot16(x, x);
+        Row16 yw;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) yw.v[j] = mul_f32x2(y.v[j], w.v[j]);
+        float sy = dot16(x, yw);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          sy += __shfl_xor_sync(0xffffffffu, sy, o);
+        }
         // absent rows (zeros) add nothing, with eps = 0 too (there r is infinite)
-        const float r = live && h < h1 ? rsqrtf(ss * (1.f / kD) + a.eps) : 0.f;
+        const float r = hb + u < n_h ? rsqrtf(ss * (1.f / kD) + a.eps) : 0.f;
         // dx = r (dz w) - x r^3 mean(dz w x)
         const float m = sy * r * (1.f / kD);
         const uint64_t r2 = dup_f32x2(r), f2 = dup_f32x2(-r * r * m);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
           g.v[j] = fma_f32x2(y.v[j], mul_f32x2(x.v[j], r2), g.v[j]);
           x.v[j] = fma_f32x2(x.v[j], f2, mul_f32x2(yw.v[j], r2));
         }
-        if (live && h < h1)
-          store_row<kInter>(dst + h * a.ds_h[kind], lp, pack8<kInter>(x));
+        if (hb + u < n_h) {
+          uint4 o0, o1;
+          pack16<kInter>(x, o0, o1);
+          __nv_bfloat16* d = dst + (hb + u) * a.ds_h[kind];
+          *reinterpret_cast<uint4*>(d + lp.o0) = o0;
+          *reinterpret_cast<uint4*>(d + lp.o1) = o1;
+        }
       }
     }
   }
+  // queries: what was put away at the change of kind, or what is at hand
   for (int k = 0; k < 2; ++k) {
-    __syncthreads();
+    if (k == 0) {
+      if (cur == 0) put(g);
+    } else {
+      if (cur == 0)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float t[2];
-      unpack_f32x2(k == 0 ? (cur == 0 ? g.v[j] : dwq.v[j]) : (cur == 0 ? 0ull : g.v[j]), t[0],
-                   t[1]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // feature of element 2 j + e: the arrangement of Row8 undone
-        const int i = 2 * (j & 1) + e;              // pair of the lane
-        const int f = kInter ? lp.o0 + 2 * i + (j >> 1) : (j < 2 ? lp.o0 : lp.o1) + i;
-        red[grp][f] = t[e];
-      }
+        for (int j = 0; j < 8; ++j) g.v[j] = 0ull;
+      put(g);
     }
     __syncthreads();
     if (threadIdx.x < kD) {
@@ -423,6 +562,7 @@ __global__ void __launch_bounds__(kNrBwdThreads, 2)
       for (int r = 0; r < kGroups; ++r) t += red[r][threadIdx.x];
       p.part[((int64_t)blockIdx.x * 2 + k) * kD + threadIdx.x] = t;
     }
+    __syncthreads();
   }
 }
 
@@ -431,6 +571,7 @@ __global__ void __launch_bounds__(1024)
     norm_rope_dw_kernel(const float* __restrict__ part, int32_t n_blocks, int32_t d,
                         float* __restrict__ dw_q, float* __restrict__ dw_k) {
   __shared__ float red[32][33];
+  grid_wait();
   const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;                    // 0 .. 2 d - 1
   float t = 0.f;
@@ -501,7 +642,7 @@ static void pick_bwd(const NormRopeBwdArgs& p, bool inter, bool f32, unsigned gr
 
 cudaError_t launch_norm_rope_bwd(NormRopeBwdArgs p, int32_t d, bool inter, bool f32, float* dw_q,
                                  float* dw_k, cudaStream_t st) {
-  const int groups = kNrBwdThreads / (d / 8);
+  const int groups = kNrBwdThreads / (d / 16);
   split_heads(p.f, 2, 8);
   if (p.f.n_items < (int64_t)kNrBwdBlocks * groups * 4) split_heads(p.f, 2, 2);
   if (p.f.n_items > 0x7FFFFF00) return cudaErrorInvalidValue;
@@ -510,8 +651,8 @@ cudaError_t launch_norm_rope_bwd(NormRopeBwdArgs p, int32_t d, bool inter, bool 
   else pick_bwd<64>(p, inter, f32, grid, st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  norm_rope_dw_kernel<<<2 * d / 32, 1024, 0, st>>>(p.part, (int32_t)grid, d, dw_q, dw_k);
-  return cudaGetLastError();
+  return launch_dependent(norm_rope_dw_kernel, 2 * d / 32, 1024, 0, st, p.part, (int32_t)grid, d,
+                          dw_q, dw_k);
 }
 
 }  // namespace msa

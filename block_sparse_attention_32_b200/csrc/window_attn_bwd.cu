@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(256)
                            int2* __restrict__ table, int32_t* __restrict__ pbase,
                            int32_t* __restrict__ counter, int32_t chunk, int32_t nblk) {
   const int lane = threadIdx.x & 31;
+  grid_launch_dependents();
   if (blockIdx.x + 1 < gridDim.x) {
     const uint32_t H = (uint32_t)(a.G * a.R), n = (uint32_t)a.n_q;
     const uint32_t rows = (uint32_t)a.batch * n * H;
@@ -272,6 +273,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const WindowArgs& a = p.w;
   int32_t* err = a.err;
+  grid_launch_dependents();
 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -337,6 +339,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
       }
+      grid_wait();                           // the work list and its counter are written
       uint32_t n = 0, ni = 0, issued[2] = {0, 0};   // streamed tiles, items with tiles
       bool ok = true;
       WbItem it{};
@@ -512,6 +515,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       __syncwarp();
     } else {
       // ---------------- -lse log2 e and -D of the query rows: streamed (dk, dv), or the item's own (dq) ----------------
+      grid_wait();                           // and so is D
       uint32_t n = 0;                        // slots filled: one per tile, or per dq item
       bool ok = true;
       for (uint32_t k = 0; ok && next_item(k); ++k) {
@@ -746,6 +750,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
 // thread.  blockIdx.x: (batch, group, key block of the cut ones' range).
 __global__ void __launch_bounds__(256)
     window_bwd_join_kernel(const __grid_constant__ WindowBwdArgs p, int32_t c_lo, int32_t n_c) {
+  grid_wait();
   const WindowArgs& a = p.w;
   const int32_t bg = blockIdx.x / n_c, c = c_lo + blockIdx.x - bg * n_c;
   int32_t first, count;
@@ -812,15 +817,12 @@ cudaError_t launch_window_attn_bwd(const CUtensorMap& tm_q, const CUtensorMap& t
   window_bwd_prep_kernel<<<(unsigned)((rows + kWbPrepRows - 1) / kWbPrepRows + 1), 256, 0, st>>>(
       a, delta, table, pbase, p.counter, pl.chunk, p.nblk);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  window_attn_bwd_kernel<<<(unsigned)min64(p.n_all, sms), kWbThreads, kWbSmemBytes, st>>>(
-      tm_q, tm_do, tm_k, tm_v, tm_k32, tm_v32, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (pl.n_part > 0) {
-    const int32_t n_c = (int32_t)(pl.c_hi - pl.c_lo);
-    window_bwd_join_kernel<<<dim3((unsigned)(a.batch * a.G * n_c), 32), 256, 0, st>>>(
-        p, (int32_t)pl.c_lo, n_c);
-  }
-  return cudaGetLastError();
+  e = launch_dependent(window_attn_bwd_kernel, (unsigned)min64(p.n_all, sms), kWbThreads,
+                       kWbSmemBytes, st, tm_q, tm_do, tm_k, tm_v, tm_k32, tm_v32, p);
+  if (e != cudaSuccess || pl.n_part == 0) return e;
+  const int32_t n_c = (int32_t)(pl.c_hi - pl.c_lo);
+  return launch_dependent(window_bwd_join_kernel, dim3((unsigned)(a.batch * a.G * n_c), 32), 256, 0,
+                          st, p, (int32_t)pl.c_lo, n_c);
 }
 
 }  // namespace msa
