@@ -30,8 +30,9 @@
 // at work; then P(n) and dS(n) (bf16) over that, the A operands of the sums.  Tiles
 // alternate between the buffers, so the sums of n - 1 and S(n + 1) run beside the
 // softmax of n.  (With one buffer for S and P, another for dP and dS, S(n + 1) had to
-// wait for dV(n): 4300 clocks a tile.)  Per tile: dP(n), dK(n-1), dV(n-1), S(n+1);
-// Q and dO slots are freed apart, Q first, since S(n + 2) needs only that.
+// wait for dV(n): 4300 clocks a tile.)  Per tile: dP(n), dK(n-1), dV(n-1), S(n+1).
+// Q and dO (K and V) slots are freed apart: three for the first, which S needs early
+// and dK keeps late, two for the second.
 // A key block that many queries see (sinks; no window) is cut into chunks of
 // query tiles whose fp32 sums a last kernel adds in chunk order.
 #include <type_traits>
@@ -51,19 +52,21 @@ constexpr int kWbRegsAtLaunch = 96, kWbRegsControl = 64, kWbRegsMath = 104;
 static_assert(kWbRegsControl + 4 * kWbRegsMath == 5 * kWbRegsAtLaunch,
               "warpgroup register shares must add up to the launch allocation");
 constexpr int kWbOffStay = 0;                          // K, V or Q, dO: 32 KB each
-constexpr int kWbOffStream = 65536;                    // two slots of 64 KB
-constexpr int kWbOffMeta = kWbOffStream + 2 * 65536;   // slots of -lse log2 e [128], -D [128]
-constexpr int kWbMeta = 4;                             // fetched this many tiles ahead
+constexpr int kWbOffStream = 65536;                    // 3 slots for Q or K, 2 for dO or V
+constexpr int kWbSlots = 5;
+constexpr int kWbOffMeta = kWbOffStream + kWbSlots * 32768;   // slots of -lse log2 e [128], -D [128]
+constexpr int kWbMeta = 2;
 constexpr int kWbOffBar = kWbOffMeta + kWbMeta * 1024;
 enum {
   XB_ITEM_FULL = 0, XB_ITEM_EMPTY = 2, XB_STAY_FULL = 4, XB_STAY_EMPTY, XB_STR_FULL = 6,
-  XB_STR_EMPTY = 10, XB_DS_FULL = 14, XB_DONE = 16, XB_META_FULL = 18,
+  XB_STR_EMPTY = XB_STR_FULL + kWbSlots, XB_DS_FULL = XB_STR_EMPTY + kWbSlots,
+  XB_DONE = XB_DS_FULL + 2, XB_META_FULL = XB_DONE + 2,
   XB_META_EMPTY = XB_META_FULL + kWbMeta, XB_S_FULL = XB_META_EMPTY + kWbMeta, XB_S_READ, XB_DP_FULL, XB_ACC_FULL, XB_ACC_EMPTY, XB_DRAIN, XB_COUNT = XB_DRAIN + 2
 };
 constexpr int kWbOffMisc = kWbOffBar + XB_COUNT * 8;
 constexpr int kWbOffItem = (kWbOffMisc + 16 + 15) / 16 * 16;    // two slots
-constexpr int kWbItemBytes = 160;
-constexpr int kWbSmemBytes = 1024 + kWbOffItem + 2 * kWbItemBytes;
+constexpr int kWbItemBytes = 112;
+constexpr int kWbSmemBytes = kWbOffItem + 2 * kWbItemBytes;
 static_assert(kWbSmemBytes <= 232448, "shared memory per block");
 constexpr int kWbItemReaders = 19;     // warps that read an item's number: all but the scheduler
 constexpr int kWbMinChunk = 32;        // query tiles of a chunk at least
@@ -264,9 +267,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
                            const __grid_constant__ CUtensorMap tm_k32,
                            const __grid_constant__ CUtensorMap tm_v32,
                            const __grid_constant__ WindowBwdArgs p) {
-  extern __shared__ uint8_t smem_raw[];
-  // (an offset, so that the compiler still knows the address space)
-  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = smem_raw;
   uint64_t* bar = reinterpret_cast<uint64_t*>(base + kWbOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + kWbOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + kWbOffMisc + 4);
@@ -279,12 +281,12 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar + XB_ITEM_FULL + s, 1);
       mbar_init(bar + XB_ITEM_EMPTY + s, kWbItemReaders);
-      for (int h = 0; h < 2; ++h) {                 // slot s: Q or K at 2 s, dO or V at 2 s + 1
-        mbar_init(bar + XB_STR_FULL + 2 * s + h, 1);
-        mbar_init(bar + XB_STR_EMPTY + 2 * s + h, 1);
-      }
       mbar_init(bar + XB_DS_FULL + s, 16);          // a lane of each warp
       mbar_init(bar + XB_DONE + s, 1);
+    }
+    for (int s = 0; s < kWbSlots; ++s) {
+      mbar_init(bar + XB_STR_FULL + s, 1);
+      mbar_init(bar + XB_STR_EMPTY + s, 1);
     }
     for (int s = 0; s < kWbMeta; ++s) {
       mbar_init(bar + XB_META_FULL + s, 1);
@@ -318,6 +320,9 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(bar + id);
   };
+  // slot and use of streamed tile m: half 0 (Q or K) goes round three, half 1 two
+  auto slot_of = [](int h, uint32_t m) { return h ? 3 + (int)(m & 1) : (int)(m % 3); };
+  auto use_of = [](int h, uint32_t m) { return h ? m >> 1 : m / 3; };
   auto item_slot = [&](uint32_t k) -> WbItem& {
     return *reinterpret_cast<WbItem*>(base + kWbOffItem + (int)(k & 1) * kWbItemBytes);
   };
@@ -371,8 +376,9 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         ++ni;
         for (int32_t t = 0; t < it.nt; ++t, ++n) {
           for (int h = 0; ok && h < 2; ++h) {
-            const int s = 2 * (int)(n & 1) + h;
-            ok = n < 2 || W(XB_STR_EMPTY + s, (n >> 1) - 1);
+            const int s = slot_of(h, n);
+            const uint32_t use = use_of(h, n);
+            ok = use == 0 || W(XB_STR_EMPTY + s, use - 1);
             if (ok && lane == 0) {
               mbar_arrive_expect_tx(bar + XB_STR_FULL + s, 32768u);
               uint8_t* dst = base + kWbOffStream + s * 32768;
@@ -391,8 +397,9 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       // no copy may still be writing shared memory when the block exits
       if (lane == 0) {
         for (int h = 0; h < 2; ++h)
-          for (uint32_t k = issued[h] > 2 ? issued[h] - 2 : 0; k < issued[h]; ++k)
-            mbar_drain(bar + XB_STR_FULL + 2 * (int)(k & 1) + h, (k >> 1) & 1u, err);
+          for (uint32_t k = issued[h] > 3 ? issued[h] - 3 : 0; k < issued[h]; ++k)
+            if (k + (h ? 2 : 3) >= issued[h])
+              mbar_drain(bar + XB_STR_FULL + slot_of(h, k), use_of(h, k) & 1u, err);
         if (ni > 0) mbar_drain(bar + XB_STAY_FULL, (uint32_t)((ni - 1) & 1), err);
       }
     } else if (warp == kWbCtl + 1) {
@@ -414,8 +421,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       // sequence are cleared: they may hold anything, and their P and dS are 0, but
       // 0 * NaN is not.  (V needs none: a column of dP that nobody sees is dropped.)
       auto landed = [&](const WbItem& it, int h, int32_t t, uint32_t m) {
-        const int s = 2 * (int)(m & 1) + h;
-        if (!W(XB_STR_FULL + s, m >> 1)) return false;
+        const int s = slot_of(h, m);
+        if (!W(XB_STR_FULL + s, use_of(h, m))) return false;
         if (a.kv_len != nullptr && it.len < a.n_kv && (it.dkv || h == 0)) {
           uint8_t* rows = base + kWbOffStream + s * 32768;
           if (it.dkv)
@@ -432,7 +439,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         if (m >= 2 && !W(XB_DONE + (int)(m & 1), (m >> 1) - 1)) return false;
         tc_fence_after();
         if (elect_one()) {
-          product(tmem + 128 * (m & 1), sa, str + (m & 1) * 65536);
+          product(tmem + 128 * (m & 1), sa, str + slot_of(0, m) * 32768);
           umma_commit(bar + XB_S_FULL);
         }
         __syncwarp();
@@ -450,9 +457,9 @@ __global__ void __launch_bounds__(kWbThreads, 1)
           tc_fence_after();
           if (elect_one()) {
             const uint32_t b = n & 1;
-            product(tmem + 128 * b, sa + 32768, str + b * 65536 + 32768);
+            product(tmem + 128 * b, sa + 32768, str + slot_of(1, n) * 32768);
             umma_commit(bar + XB_DP_FULL);
-            if (!dkv) umma_commit(bar + XB_STR_EMPTY + 2 * b + 1);      // V's last use
+            if (!dkv) umma_commit(bar + XB_STR_EMPTY + slot_of(1, n));  // V's last use
             if (t + 1 == nt) umma_commit(bar + XB_STAY_EMPTY);
           }
           __syncwarp();
@@ -488,18 +495,19 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         if (nt == 0) continue;
         if (ni > 0 && !W(XB_ACC_EMPTY, ni - 1)) { ok = false; break; }
         for (int32_t t = 0; t < nt; ++t, ++n) {
-          const uint32_t b = n & 1, str = str0 + b * 65536, x = tmem + 128 * b;
+          const uint32_t b = n & 1, x = tmem + 128 * b;
+          const int s0 = slot_of(0, n), s1 = slot_of(1, n);
           // the tiles it reads (landed long ago; V's slot may have been refilled)
-          if (!W(XB_STR_FULL + 2 * (int)b, n >> 1)) { ok = false; break; }
-          if (dkv && !W(XB_STR_FULL + 2 * (int)b + 1, n >> 1)) { ok = false; break; }
+          if (!W(XB_STR_FULL + s0, use_of(0, n))) { ok = false; break; }
+          if (dkv && !W(XB_STR_FULL + s1, use_of(1, n))) { ok = false; break; }
           if (!W(XB_DS_FULL + (int)b, n >> 1)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
-            product(tmem + 384, x + 16, str, t > 0);
-            umma_commit(bar + XB_STR_EMPTY + 2 * b);
+            product(tmem + 384, x + 16, str0 + s0 * 32768, t > 0);
+            umma_commit(bar + XB_STR_EMPTY + s0);
             if (dkv) {
-              product(tmem + 256, x, str + 32768, t > 0);
-              umma_commit(bar + XB_STR_EMPTY + 2 * b + 1);
+              product(tmem + 256, x, str0 + s1 * 32768, t > 0);
+              umma_commit(bar + XB_STR_EMPTY + s1);
             }
             umma_commit(bar + XB_DONE + b);
             if (t + 1 == nt) umma_commit(bar + XB_ACC_FULL);
