@@ -49,11 +49,11 @@ static_assert(kWaRegsControl + 2 * kWaRegsSoftmax == 3 * kWaRegsAtLaunch,
 constexpr int kWaRing = 5;                              // 32 KB K or V tiles in flight
 constexpr int kWaOffQ = 0;                              // Q_A, Q_B
 constexpr int kWaOffRing = 65536;
-constexpr int kWaOffML = kWaOffRing + kWaRing * 32768;  // m, l of half B's rows
-constexpr int kWaOffBar = kWaOffML + 1024;
+constexpr int kWaOffML = 32768;      // m, l of both halves' rows when they share a tile (Q_B is unused)
+constexpr int kWaOffBar = kWaOffRing + kWaRing * 32768;
 enum {
   WB_Q_FULL = 0, WB_Q_EMPTY = 2, WB_S_FULL = 4, WB_P_FULL = 6, WB_PV_DONE = 8, WB_O_EMPTY = 10,
-  WB_S_READ = 12, WB_JOIN, WB_KV_FULL, WB_KV_EMPTY = WB_KV_FULL + kWaRing,
+  WB_S_READ = 12, WB_JOIN, WB_KV_FULL = WB_JOIN + 2, WB_KV_EMPTY = WB_KV_FULL + kWaRing,
   WB_DRAIN = WB_KV_EMPTY + kWaRing, WB_ITEM_FULL = WB_DRAIN + 2, WB_ITEM_EMPTY = WB_ITEM_FULL + 2,
   WB_COUNT = WB_ITEM_EMPTY + 2
 };
@@ -63,10 +63,18 @@ constexpr int kWaSmemBytes = 1024 + kWaOffItem + 2 * (int)sizeof(WinItem);
 constexpr int kWaItemReaders = 10;                      // warps 0-7, 9, 10
 static_assert(kWaSmemBytes <= 232448, "shared memory per block");
 // the 8 bits of x behind its bf16 rounding b (as fp32 bits): a signed count of 2^8
-// fp32 units from b
-__device__ __forceinline__ uint32_t rest_bits(float x, uint32_t b) {
-  const int32_t d = (int32_t)(__float_as_uint(x) - b);
-  return (uint32_t)max(-128, min(127, (d + 128) >> 8)) & 0xFFu;
+// fp32 units from b; of two values, above the low half of c
+__device__ __forceinline__ uint32_t rest_pair(float x0, float x1, uint32_t pk, uint32_t c) {
+  const int32_t d0 = (int32_t)(__float_as_uint(x0) - (pk << 16) + 128u) >> 8;
+  const int32_t d1 = (int32_t)(__float_as_uint(x1) - (pk & 0xFFFF0000u) + 128u) >> 8;
+  uint32_t r;
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(d1), "r"(d0), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ void st_words_v8(void* p, const uint32_t* w) {
+  st_global_v8(static_cast<float*>(p), u2f(w[0]), u2f(w[1]), u2f(w[2]), u2f(w[3]), u2f(w[4]),
+               u2f(w[5]), u2f(w[6]), u2f(w[7]));
 }
 constexpr float kLazyLog2 = 8.f;     // rescale O when a row's maximum grows by more than 2^8
 }  // namespace
@@ -87,7 +95,17 @@ __global__ void __launch_bounds__(kWaThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + kWaOffMisc + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int32_t* err = a.err;
+  const bool split = tiles_per_item == 1;              // the halves share one row tile
 
+  WinItem it0{};                             // the first item, decoded while the barriers are made
+  if (warp == 8) {
+    if (lane == 0) {
+      prefetch_tensormap(&tm_q);
+      prefetch_tensormap(&tm_k);
+      prefetch_tensormap(&tm_v);
+    }
+    win_item(it0, a, (int32_t)blockIdx.x, tiles_per_item);
+  }
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar + WB_Q_FULL + x, 1);
@@ -95,14 +113,14 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       mbar_init(bar + WB_S_FULL + x, 1);
       mbar_init(bar + WB_P_FULL + x, 4);           // a lane of each warp
       mbar_init(bar + WB_PV_DONE + x, 1);
-      mbar_init(bar + WB_O_EMPTY + x, 4);
+      mbar_init(bar + WB_O_EMPTY + x, split ? 8 : 4);
+      mbar_init(bar + WB_JOIN + x, 4);
     }
     for (int s = 0; s < kWaRing; ++s) {
       mbar_init(bar + WB_KV_FULL + s, 1);
       mbar_init(bar + WB_KV_EMPTY + s, 1);
     }
     mbar_init(bar + WB_S_READ, 4);
-    mbar_init(bar + WB_JOIN, 4);
     mbar_init(bar + WB_DRAIN, 1);
     mbar_init(bar + WB_DRAIN + 1, 1);
     for (int s = 0; s < 2; ++s) {
@@ -129,7 +147,6 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(bar + id);
   };
-  const bool split = tiles_per_item == 1;              // the halves share one row tile
   // Items are decoded once, by the TMA warp, and kept in shared memory: the softmax
   // warps need their registers.  `cur`: the role's item
   auto item_slot = [&](uint32_t k) {
@@ -159,13 +176,8 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     setmaxnreg_dec<kWaRegsControl>();
   if (warp == 8) {
     // ---------------- TMA ----------------
-    if (lane == 0) {
-      prefetch_tensormap(&tm_q);
-      prefetch_tensormap(&tm_k);
-      prefetch_tensormap(&tm_v);
-    }
     uint32_t nq[2] = {0, 0}, n = 0;          // Q loads per tile, ring slots
-    WinItem it{};
+    WinItem it = it0;
     bool ok = true;
     auto push = [&](const CUtensorMap* tm, const CUtensorMap* tm32, int j) {
       const uint32_t s = n % kWaRing;
@@ -184,7 +196,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       const int64_t i = (int64_t)k * gridDim.x + at;
       if (k >= 2 && !W(WB_ITEM_EMPTY + (int)(k & 1), (k >> 1) - 1)) break;
       const bool end = i >= n_items;
-      if (!end) win_item(it, a, (int32_t)i, tiles_per_item);
+      if (k > 0 && !end) win_item(it, a, (int32_t)i, tiles_per_item);
       if (lane == 0) {
         *item_slot(k) = it;
         if (end) item_slot(k)->nt = -1;
@@ -333,7 +345,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     const uint64_t scale2 = pack_f32x2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
     const int32_t tpt = 128 / a.R;            // tokens per row tile
     const int32_t sink = (int32_t)a.sink;
-    float2* ml_b = reinterpret_cast<float2*>(base + kWaOffML);
+    float2* ml = reinterpret_cast<float2*>(base + kWaOffML);   // [half][row]
     uint32_t ns = 0, np = 0, np_other = 0, nj = 0;
     bool ok = true;
     for (uint32_t ki = 0; ok && next_item(ki); ++ki) {
@@ -441,70 +453,83 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         if (!W(WB_PV_DONE + x, np - 1)) { ok = false; break; }
         tc_fence_after();
       }
-      // shared row tile with two key tiles or more: half B hands over its (m, l), half A
-      // reads B's accumulators from the same TMEM lanes
+      // shared row tile: the halves exchange (m, l); each stores half of the columns
       float fa = 1.f, fb = 0.f;
-      bool both = false;
-      if (split && it.nt > 1) {
-        if (x == 1) {
-          ml_b[row] = make_float2(m, l);
-          arrive(WB_JOIN);
-          done_item(ki);
-          continue;                            // A frees B's accumulators
-        }
-        if (!W(WB_JOIN, nj)) { ok = false; break; }
+      if (split) {
+        ml[128 * x + row] = make_float2(m, l);
+        arrive(WB_JOIN + x);
+        if (!W(WB_JOIN + (x ^ 1), nj)) { ok = false; break; }
         ++nj;
-        np_other += it.nt >> 1;                // half B's products: every second tile
-        if (!W(WB_PV_DONE + 1, np_other - 1)) { ok = false; break; }
+        const int n_other = (it.nt + x) >> 1;              // its products: every second tile
+        np_other += n_other;
+        if (n_other > 0 && !W(WB_PV_DONE + (x ^ 1), np_other - 1)) { ok = false; break; }
         tc_fence_after();
-        const float2 o = ml_b[row];
-        const float mm = fmaxf(m, o.x), z = mm == -INFINITY ? 0.f : mm;
-        fa = ex2_approx(m - z);
-        fb = ex2_approx(o.x - z);
-        l = l * fa + o.y * fb;
-        m = mm;
-        both = true;
+        const float2 ma = ml[row], mb = ml[128 + row];
+        m = fmaxf(ma.x, mb.x);
+        const float z = m == -INFINITY ? 0.f : m;
+        fa = ex2_approx(ma.x - z);
+        fb = ex2_approx(mb.x - z);
+        l = ma.y * fa + mb.y * fb;
       }
       // the item's rows leave: o = O / l
-      const bool store = i_row < a.n_q && !(split && x == 1);
-      const bool live = store && t < it.len && begun;
+      const bool has = split ? it.nt > 0 : begun, both = split && it.nt > 1;
+      const bool store = i_row < a.n_q;
+      const bool live = store && t < it.len && has;
       const int64_t orow =
           ((int64_t)it.b * a.n_q + i_row) * ((int64_t)a.G * a.R) + (int64_t)it.g * a.R + row % a.R;
       const float inv = live && l != 0.f ? 1.f / l : 0.f;
+      const float f = both ? 1.f : fa * inv;
       fa *= inv;
       fb *= inv;
-      if (store) a.lse[orow] = live ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+      if (store && !(split && x == 1))
+        a.lse[orow] = live ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+      const uint32_t ta = split ? lanes + kColO : to;
+      const int c0 = split ? 2 * x : 0, c1 = split ? c0 + 2 : 4;
 #pragma unroll 1
-      for (int cc = 0; cc < 8; ++cc) {
-        uint32_t r[16], rb[16];
-        if (begun) tmem_ld_32x32b_x16(to + 16 * cc, r);
-        if (both) tmem_ld_32x32b_x16(to + 128 + 16 * cc, rb);
+      for (int cc = c0; cc < c1; ++cc) {
+        uint32_t r[32];
+        if (has) tmem_ld_32x32b_x32(ta + 32 * cc, r);
         tmem_ld_wait();
-        if (store) {
-          uint32_t pk[8], rest[4] = {0u, 0u, 0u, 0u};
+        if (both) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            float u = live ? u2f(r[2 * q]) * fa : 0.f, v = live ? u2f(r[2 * q + 1]) * fa : 0.f;
-            if (both && live) {
-              u += u2f(rb[2 * q]) * fb;
-              v += u2f(rb[2 * q + 1]) * fb;
-            }
-            pk[q] = pack_bf16x2(u, v);
-            if (a.rest != nullptr)
-              rest[q >> 1] |= (rest_bits(u, pk[q] << 16) | rest_bits(v, pk[q] & 0xFFFF0000u) << 8)
-                              << (16 * (q & 1));
+          for (int h = 0; h < 2; ++h) {
+            uint32_t rb[16];
+            tmem_ld_32x32b_x16(ta + 128 + 32 * cc + 16 * h, rb);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              r[16 * h + q] = f2u(u2f(r[16 * h + q]) * fa + u2f(rb[q]) * fb);
           }
-          if (a.rest != nullptr)
-            *reinterpret_cast<uint4*>(a.rest + orow * kHeadDim + 16 * cc) =
-                make_uint4(rest[0], rest[1], rest[2], rest[3]);
-          st_global_v8(reinterpret_cast<float*>(a.out + orow * kHeadDim + 16 * cc), u2f(pk[0]),
-                       u2f(pk[1]), u2f(pk[2]), u2f(pk[3]), u2f(pk[4]), u2f(pk[5]), u2f(pk[6]),
-                       u2f(pk[7]));
+        }
+        if (store) {
+          uint32_t pk[16], rest[8];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const float u = live ? u2f(r[2 * q]) * f : 0.f, v = live ? u2f(r[2 * q + 1]) * f : 0.f;
+            pk[q] = pack_bf16x2(u, v);
+            r[2 * q] = f2u(u);
+            r[2 * q + 1] = f2u(v);
+          }
+          st_words_v8(a.out + orow * kHeadDim + 32 * cc, pk);
+          st_words_v8(a.out + orow * kHeadDim + 32 * cc + 16, pk + 8);
+          if (a.rest != nullptr) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              rest[q] = rest_pair(u2f(r[4 * q]), u2f(r[4 * q + 1]), pk[2 * q],
+                                  rest_pair(u2f(r[4 * q + 2]), u2f(r[4 * q + 3]), pk[2 * q + 1], 0u));
+            uint4* ro = reinterpret_cast<uint4*>(a.rest + orow * kHeadDim + 32 * cc);
+            ro[0] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+            ro[1] = make_uint4(rest[4], rest[5], rest[6], rest[7]);
+          }
         }
       }
       tc_fence_before();
-      if (begun) arrive(WB_O_EMPTY + x);
-      if (both) arrive(WB_O_EMPTY + 1);
+      if (split) {
+        if (has) arrive(WB_O_EMPTY);
+        if (both) arrive(WB_O_EMPTY + 1);
+      } else if (begun) {
+        arrive(WB_O_EMPTY + x);
+      }
       done_item(ki);
     }
   }

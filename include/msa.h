@@ -20,7 +20,9 @@
  * Beside the path: an 8-bit (e4m3) index branch, the selection recall / KL
  * alignment target of the index branch, token-level selection at the same
  * key budget, and the backward of the attention (dq, dk, dv) for training
- * through the sparse attention.
+ * through the sparse attention.  Around it: per-head norms with the position
+ * rotation (dense, into a paged cache, backward), attention of one new token
+ * over a paged cache, and window attention with sinks (forward, backward).
  *
  * Conventions for every entry point:
  *   - All pointers are DEVICE pointers unless stated; the caller owns every
@@ -34,6 +36,7 @@
  *     that ran past its time limit) stores an MSA_DEVERR_* code there and
  *     returns early.  Nothing traps.
  *   - Results are deterministic: bit-identical from run to run.
+ *     Calls that may overlap on the GPU need a workspace each.
  *   - Fixed sizes: block B_k = 128 tokens, top-k = 16 blocks (own included),
  *     head_dim = 128, d_idx in {64, 128}.
  *   - Layouts are given as [outer, ..., inner]; the innermost dimension is
