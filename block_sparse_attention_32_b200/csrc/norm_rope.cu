@@ -10,15 +10,19 @@
 //   dw = sum over rows dz * xh,   dx = (dz w - xh mean(dz w xh)) / sqrt(...).
 //
 // Bound: HBM -- every value is read once and written once (2 + 2 bytes per
-// feature forward, 2 + 2 or 4 + 2 backward).  A row lives in D / 8 lanes of 8
-// features each.  For pairs (i, i + rot / 2) a lane takes features 4 l .. 4 l + 3 of
-// both halves (two 8-byte loads), so that both partners of every pair are its
-// own and the rotation needs no exchange; the features behind rot go to the
-// lanes left over.  Only the sum of squares (and, backward, one more sum) crosses
-// lanes.  The D / 8 lanes keep one token and walk `hc` of its heads: the token's
+// feature forward, 4 + 2 or 6 + 2 backward).  A row lives in D / 8 lanes of 8
+// features each (backward: D / 16 of 16).  For pairs (i, i + rot / 2) a lane takes
+// features 4 l .. 4 l + 3 of both halves (two 8-byte loads), so that both partners of
+// every pair are its own and the rotation needs no exchange; the features behind rot
+// go to the lanes left over.  Only the sum of squares (and, backward, one more sum)
+// crosses lanes.  A row's lanes keep one token and walk `hc` of its heads: the token's
 // cosines and sines (fp32, the size of two bf16 rows) are read once per hc heads
 // and kept in registers.  Everything is computed in fp32 and rounded to bf16 once,
 // at the store.
+// Measured: forward, 32768 tokens x (32 + 8) heads of 128: 110 us, 688 MB, 6.2 TB/s
+// (0.95 of the copy rate).  Backward, 16384 x (64 + 8), bf16 gradients: 160 us, 915
+// MB, 5.7 TB/s (0.87; the shuffles, unpacking and the two sums a row keep it from the
+// rest).  64 tokens of a decode step into their pages: 5 us, a launch and a latency.
 #include "common.cuh"
 #include "layer_args.cuh"
 
@@ -613,8 +617,9 @@ static void split_heads(NormRopeArgs& a, int kinds, int hc) {
 cudaError_t launch_norm_rope(NormRopeArgs a, int32_t d, bool inter, bool paged,
                              cudaStream_t st) {
   const int kinds = paged ? 3 : 2, groups = kNrThreads / (d / 8);
-  // eight heads per token's angles when that still fills the GPU; two when it
-  // does not, so that a decode step spreads over more SMs
+  // eight heads per token's angles when that still fills the GPU (2048 tokens x 40
+  // heads: 14.4 us, with two 20.5); two when it does not, so that a decode step spreads
+  // over more SMs (64 tokens: 6.2 us, with eight 8.2)
   split_heads(a, kinds, kNrHeads);
   if (a.n_items < (int64_t)148 * 4 * groups) split_heads(a, kinds, 2);
   if (a.n_items > 0x7FFFFF00) return cudaErrorInvalidValue;
@@ -643,6 +648,8 @@ static void pick_bwd(const NormRopeBwdArgs& p, bool inter, bool f32, unsigned gr
 cudaError_t launch_norm_rope_bwd(NormRopeBwdArgs p, int32_t d, bool inter, bool f32, float* dw_q,
                                  float* dw_k, cudaStream_t st) {
   const int groups = kNrBwdThreads / (d / 16);
+  // eight heads or two, as forward, by the blocks that stay (64 tokens x 40 heads: 10.3
+  // us with two, 14.4 with eight; 2048: 24.6 and 28; 16384 x 72: eight is the faster)
   split_heads(p.f, 2, 8);
   if (p.f.n_items < (int64_t)kNrBwdBlocks * groups * 4) split_heads(p.f, 2, 2);
   if (p.f.n_items > 0x7FFFFF00) return cudaErrorInvalidValue;

@@ -29,7 +29,13 @@
 // The running maximum is kept until a row exceeds it by 2^8: then O is
 // rescaled by the softmax warps themselves, after P V of the tile before.
 // Exact: P and l use the same maximum.
-// P is rounded to bf16 (2^-9 relative a weight) for the product; l sums fp32.
+// P is rounded to bf16 (at most 2^-8 of a weight) for the product; l sums fp32.
+// Rows leave 32 columns at a time straight from TMEM: the lanes' rows are whole
+// 64-byte runs.
+// Measured: 32768 tokens, 32 / 8 heads, W = 4096, S = 64 (2.09 PFLOP): 1600 us, 1.31
+// PFLOP/s (0.80 of the burst rate; long runs meet the power cap: 1900 us).  8192
+// tokens, 64 / 8 heads, W = 1024: 310 us.  4096 tokens, 4 / 1 heads, W = 512: 16 us,
+// 12 of them on the SM: 3 until the first tile is there, 2 x 3 tiles a half.
 #include <type_traits>
 
 #include "common.cuh"

@@ -525,7 +525,7 @@ MSA_API msa_status msa_paged_decode_attn(const msa_dims* dims, int64_t window, i
  *   out_rest  [B, n_q, h_q, 128] int8 (16-byte aligned), or NULL: the 8 bits behind
  *          each bf16 of out, so that the fp32 with the bits (out << 16) + (rest << 8)
  *          is o to 2^-17.  The backward's D = dO.o takes it: from the rounded out
- *          alone D is off by up to 2^-9 sum |dO o|, which reaches dq and dk.
+ *          alone D is off by up to 2^-8 sum |dO o|, which reaches dq and dk.
  * K and V must be finite at the keys below kv_len.  A stride of 0 over a dimension
  * of extent > 1 (q, k, v; d_o in the backward) is MSA_ERR_UNSUPPORTED. */
 MSA_API msa_status msa_window_attn_fwd(const msa_dims* dims, int64_t window, int64_t n_sink,
