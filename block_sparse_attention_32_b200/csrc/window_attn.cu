@@ -32,7 +32,7 @@
 // P is rounded to bf16 (at most 2^-8 of a weight) for the product; l sums fp32.
 // Rows leave 32 columns at a time straight from TMEM: the lanes' rows are whole
 // 64-byte runs.
-// Measured: 32768 tokens, 32 / 8 heads, W = 4096, S = 64 (2.09 PFLOP): 1600 us, 1.31
+// Measured: 32768 tokens, 32 / 8 heads, W = 4096, S = 64 (2.09 TFLOP): 1600 us, 1.31
 // PFLOP/s (0.80 of the burst rate; long runs meet the power cap: 1900 us).  8192
 // tokens, 64 / 8 heads, W = 1024: 310 us.  4096 tokens, 4 / 1 heads, W = 512: 16 us,
 // 12 of them on the SM: 3 until the first tile is there, 2 x 3 tiles a half.
