@@ -37,11 +37,13 @@
 // query tiles whose fp32 sums a last kernel adds in chunk order.
 // Measured: 8192 tokens, 64 / 8 heads, W = 1024, S = 4: 860 us (0.905 TFLOP of visible
 // pairs' products: 1.05 PFLOP/s, 0.64 of the burst rate) + 50 for D and the work list.
-// The tensor pipe is busy 0.55 of its cycles: a dk, dv tile's softmax takes 3100 of its 4100 clocks (S to registers 340,
-// P 1240 of which 1024 are ex2, dS 1400, the waits between the rest) with all warps at the
-// same tile, and lse and D of the streamed rows come as shared-memory broadcasts that
-// stand behind the tensor core's operand reads.  Two sets of warps taking alternate tiles
-// need 64 columns a thread: spilled, or with half the warps 1.2 times slower.
+// The tensor pipe is busy 0.55 of its cycles.  With the softmax taken out (timed, wrong
+// results) the products and their loads alone take 690 us, without the loads 625: a
+// product of two shared-memory operands needs all 128 bytes a clock of the shared memory,
+// which the loads and the broadcasts of lse and D share; the barriers alone, five a tile,
+// 355.  The exponentials and the broadcasts are not what is waited for (without either:
+// 845 of 860).  Two sets of warps taking alternate tiles need 64 columns a thread:
+// spilled, or with half the warps 1.2 times slower.
 #include <type_traits>
 
 #include "common.cuh"
