@@ -146,3 +146,65 @@ def test_prefill_into_pages_then_decode(window, sink, nhd):
                                          dense_v[:, :, :n_kv], kv_len)
     for b in range(B):
         assert _rel(out[b, 0], o_dense[b, n_all[b] - 1].double()) <= CHAIN
+
+
+def _step(seed, n=700, H=16, G=2):
+    """A layer's training step with buffers of its own: returns (run, outputs)."""
+    plan = pipeline.NormRope(pipeline.rope_table(n, 64), 1 + 0.1 * _rn(seed, 128, dtype=torch.float32))
+    xq, xk, do = _rn(seed + 1, 2, n, H, 128), _rn(seed + 2, 2, n, G, 128), _rn(seed + 3, 2, n, H, 128)
+    v = _rn(seed + 4, 2, G, n, 128)
+    q, k = torch.empty_like(xq), torch.empty_like(v)
+    win = pipeline.WindowBuffers.allocate(pipeline.window_dims(2, n, n, 0, H, G), 300, 5, backward=True)
+    grads = pipeline.NormRopeGrads.allocate(xq, xk)
+
+    def run():
+        pipeline.norm_rope(plan, xq, xk, q, k)
+        pipeline.window_forward(win, q, k, v)
+        pipeline.window_backward(win, q, k, v, do)
+        pipeline.norm_rope_backward(plan, xq, xk, win.dq, win.dk, grads)
+
+    return run, [q, k, win.out, win.lse, win.dv, grads.dx_q, grads.dx_k, grads.dw_q, win.dev_err]
+
+
+def _decode(seed, B=5, H=32, G=4):
+    cache = pipeline.PagedCache.allocate(B, 5000, G, page_size=32)
+    cache.k_pages.copy_(_rn(seed, *cache.k_pages.shape))
+    cache.v_pages.copy_(_rn(seed + 1, *cache.v_pages.shape))
+    cache.seq_lens.copy_(torch.tensor([1, 4999, 0, 317, 2048], dtype=torch.int32))
+    buf, q = pipeline.DecodeBuffers.allocate(cache, H), _rn(seed + 2, B, 1, H, 128)
+    return (lambda: pipeline.paged_decode(buf, q, cache)), [buf.out, buf.lse, buf.dev_err]
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_steps_side_by_side_on_streams(captured):
+    """Two training steps and two decode steps, each with buffers of its own, run over
+    each other on four streams, eagerly or as replayed graphs: the bits of a lone run."""
+    jobs = [_step(10), _decode(20), _step(30), _decode(40)]
+    alone = []
+    for run, outs in jobs:
+        run()
+        torch.cuda.synchronize()
+        alone.append([o.clone() for o in outs])
+        for o in outs:
+            o.fill_(77)
+        outs[-1].zero_()                                # dev_err
+    runs = [run for run, _ in jobs]
+    if captured:
+        graphs = []
+        for run in runs:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                run()
+            graphs.append(g)
+        runs = [g.replay for g in graphs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for run, s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                run()
+    torch.cuda.synchronize()
+    for (_, outs), want in zip(jobs, alone):
+        assert int(outs[-1][0]) == 0
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
