@@ -33,6 +33,8 @@
 // wait for dV(n): 4300 clocks a tile.)  Per tile: dP(n), dK(n-1), dV(n-1), S(n+1).
 // Q and dO (K and V) slots are freed apart: three for the first, which S needs early
 // and dK keeps late, two for the second.
+// Where few keys a row or few tiles are at stake, every tile comes twice, for the high and
+// the low parts of P and dS (wb_plan).
 // A key block that many queries see (sinks; no window) is cut into chunks of
 // query tiles whose fp32 sums a last kernel adds in chunk order.
 // Measured: 8192 tokens, 64 / 8 heads, W = 1024, S = 4: 860 us (0.905 TFLOP of visible
@@ -63,14 +65,15 @@ static_assert(kWbRegsControl + 4 * kWbRegsMath == 5 * kWbRegsAtLaunch,
 constexpr int kWbOffStay = 0;                          // K, V or Q, dO: 32 KB each
 constexpr int kWbOffStream = 65536;                    // 3 slots for Q or K, 2 for dO or V
 constexpr int kWbSlots = 5;
-constexpr int kWbOffMeta = kWbOffStream + kWbSlots * 32768;   // slots of -lse log2 e [128], -D [128]
+constexpr int kWbOffMeta = kWbOffStream + kWbSlots * 32768;   // slots: -lse log2 e [128], -D [128]
 constexpr int kWbMeta = 2;
 constexpr int kWbOffBar = kWbOffMeta + kWbMeta * 1024;
 enum {
   XB_ITEM_FULL = 0, XB_ITEM_EMPTY = 2, XB_STAY_FULL = 4, XB_STAY_EMPTY, XB_STR_FULL = 6,
   XB_STR_EMPTY = XB_STR_FULL + kWbSlots, XB_DS_FULL = XB_STR_EMPTY + kWbSlots,
   XB_DONE = XB_DS_FULL + 2, XB_META_FULL = XB_DONE + 2,
-  XB_META_EMPTY = XB_META_FULL + kWbMeta, XB_S_FULL = XB_META_EMPTY + kWbMeta, XB_S_READ, XB_DP_FULL, XB_ACC_FULL, XB_ACC_EMPTY, XB_DRAIN, XB_COUNT = XB_DRAIN + 2
+  XB_META_EMPTY = XB_META_FULL + kWbMeta, XB_S_FULL = XB_META_EMPTY + kWbMeta, XB_S_READ,
+  XB_DP_FULL, XB_ACC_FULL, XB_ACC_EMPTY, XB_DRAIN, XB_COUNT = XB_DRAIN + 2
 };
 constexpr int kWbOffMisc = kWbOffBar + XB_COUNT * 8;
 constexpr int kWbOffItem = (kWbOffMisc + 16 + 15) / 16 * 16;    // two slots
@@ -78,8 +81,6 @@ constexpr int kWbItemBytes = 112;
 constexpr int kWbSmemBytes = kWbOffItem + 2 * kWbItemBytes;
 static_assert(kWbSmemBytes <= 232448, "shared memory per block");
 constexpr int kWbItemReaders = 19;     // warps that read an item's number: all but the scheduler
-constexpr int kWbMinChunk = 32;        // query tiles of a chunk at least
-constexpr int kWbSplit = 2 * 148;      // chunks aimed at when blocks are cut
 
 struct WindowBwdArgs {
   WindowArgs w;
@@ -106,9 +107,12 @@ __host__ __device__ __forceinline__ int32_t wb_chunks(int32_t count, int32_t chu
   return count <= chunk ? 1 : (count + chunk - 1) / chunk;
 }
 
+constexpr int64_t kWbTwiceTiles = 64, kWbTwiceKeys = 4;   // query x key tiles; keys a row
+
 struct WbPlan {
   int64_t nblk, n_cut, n_part, c_lo, c_hi, n_dkv, n_dq;   // c_lo .. c_hi: the cut blocks' range
   int32_t chunk;
+  bool twice;
 };
 WbPlan wb_plan(const WindowArgs& a) {
   WbPlan p{};
@@ -119,7 +123,20 @@ WbPlan wb_plan(const WindowArgs& a) {
     wb_query_tiles(a, c, f, n);
     total += n;
   }
-  p.chunk = (int32_t)max64(kWbMinChunk, (total * a.batch * a.G + kWbSplit - 1) / kWbSplit);
+  total *= a.batch * a.G;
+  // Tiles twice: a sum of few terms keeps the full error of P's and dS's rounding to bf16,
+  // 2^-8 a term, beside the result's own.  Where rows see few keys, or a problem is so small
+  // that launches are its time, each tile comes twice, and the second time the sums take
+  // what the rounding of P and dS left (2^-17 remains).  A training step of 3 x 97 tokens,
+  // 8 / 1 heads, L2 cold: 48 us, once 44; 8192 tokens, 32 / 4 heads, window 8: 286 and 220,
+  // so not there.
+  p.twice = total <= kWbTwiceTiles ||
+            (a.window > 0 && min64(a.window, a.n_kv) + a.sink <= kWbTwiceKeys);
+  // Tiles of a chunk: few while SMs stand idle (512 tokens, 8 / 1 heads, no window: 4 tiles
+  // 46 us, 8: 52, 32: 83), then about 1.6 chunks an SM (1024 tokens, 16 / 2 heads: 62 us, with
+  // one an SM 69, with 32 tiles 97; 3 ragged x 1111: 109, with two an SM 115), up to 32 tiles
+  p.chunk = (int32_t)max64(max64(p.twice ? 2 : 4, min64(32, (total + 89) / 90)),
+                           (total + 295) / 296);
   p.c_lo = p.nblk;
   for (int64_t c = 0; c < p.nblk; ++c) {
     int32_t f, n;
@@ -268,6 +285,14 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// two bf16, or (low) what their rounding leaves, rounded
+__device__ __forceinline__ uint32_t pack_part(float u, float v, bool low) {
+  const uint32_t h = pack_bf16x2(u, v);
+  return low ? pack_bf16x2(u - u2f(h << 16), v - u2f(h & 0xFFFF0000u)) : h;
+}
+
+// kTwice: every streamed tile comes twice, for the high and the low parts of P and dS
+template <bool kTwice>
 __global__ void __launch_bounds__(kWbThreads, 1)
     window_attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                            const __grid_constant__ CUtensorMap tm_do,
@@ -341,6 +366,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
   };
   auto done_item = [&](uint32_t k) { arrive(XB_ITEM_EMPTY + (int)(k & 1)); };
   const int32_t tpt = 128 / a.R;             // tokens per query tile
+  auto tile_of = [](int32_t t) { return kTwice ? t >> 1 : t; };    // of step t
   const float log2e = 1.4426950408889634f;
 
   if (warp >= kWbCtl) {
@@ -368,6 +394,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         idx = __shfl_sync(0xffffffffu, idx, 0);
         it.end = idx >= p.n_all;
         if (!it.end) wb_item(it, p, idx);
+        if (kTwice) it.nt *= 2;
         if (lane == 0) {
           item_slot(k) = it;
           mbar_arrive(bar + XB_ITEM_FULL + (int)(k & 1));
@@ -393,10 +420,10 @@ __global__ void __launch_bounds__(kWbThreads, 1)
               uint8_t* dst = base + kWbOffStream + s * 32768;
               if (it.dkv)
                 load(dst, h ? &tm_do : &tm_q, bar + XB_STR_FULL + s, it.g * a.R,
-                     (it.q_tile + t) * tpt);
+                     (it.q_tile + tile_of(t)) * tpt);
               else
                 win_load_keys(dst, h ? &tm_v : &tm_k, h ? &tm_v32 : &tm_k32,
-                              bar + XB_STR_FULL + s, it.w, t);
+                              bar + XB_STR_FULL + s, it.w, tile_of(t));
             }
             if (ok) issued[h] = n + 1;
           }
@@ -435,10 +462,11 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         if (a.kv_len != nullptr && it.len < a.n_kv && (it.dkv || h == 0)) {
           uint8_t* rows = base + kWbOffStream + s * 32768;
           if (it.dkv)
-            win_clear_rows(rows, (it.len - (int32_t)a.q_pos0 - (it.q_tile + t) * tpt) * a.R, 128,
+            win_clear_rows(rows,
+                           (it.len - (int32_t)a.q_pos0 - (it.q_tile + tile_of(t)) * tpt) * a.R, 128,
                            lane);
           else
-            win_clear_keys(rows, it.w, t, lane);
+            win_clear_keys(rows, it.w, tile_of(t), lane);
         }
         return true;
       };
@@ -531,7 +559,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       }
       __syncwarp();
     } else {
-      // ---------------- -lse log2 e and -D of the query rows: streamed (dk, dv), or the item's own (dq) ----------------
+      // ---------------- -lse log2 e, -D of the streamed rows (dk, dv) or the item's (dq) ----------------
       grid_wait();                           // and so is D
       uint32_t n = 0;                        // slots filled: one per tile, or per dq item
       bool ok = true;
@@ -545,7 +573,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const int r = 32 * u + lane;
-            const int64_t i = (int64_t)(q_tile + t) * tpt + r / a.R;
+            const int64_t i = (int64_t)(q_tile + tile_of(t)) * tpt + r / a.R;
             const bool live = i < a.n_q && a.q_pos0 + i < it.len;
             const int64_t row =
                 ((int64_t)it.b * a.n_q + i) * ((int64_t)a.G * a.R) + it.g * a.R + r % a.R;
@@ -599,7 +627,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       const int32_t sink = (int32_t)a.sink;
       // one tile; kDkv: lse and D come with the columns, P goes to the tensor core too.
       // Of its 32 columns of the buffer, P takes the first 16, dS the others
-      auto tile = [&](auto kind, uint32_t vis) {
+      auto tile = [&](auto kind, uint32_t vis, bool low, uint32_t alone) {
         constexpr bool kDkv = decltype(kind)::value;
         const bool full = __all_sync(0xffffffffu, vis == ~0u);
         const ulonglong2* m = reinterpret_cast<const ulonglong2*>(
@@ -641,9 +669,10 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         tmem_ld_32x32b_x16(ts, d);
         const uint64_t nd2 = pack_f32x2(__float_as_uint(nd), __float_as_uint(nd));
         tmem_ld_wait();
+        if (kTwice) vis &= ~alone;
         if (kDkv) {
 #pragma unroll
-          for (int q = 0; q < 16; ++q) pk[q] = pack_bf16x2(u2f(s[2 * q]), u2f(s[2 * q + 1]));
+          for (int q = 0; q < 16; ++q) pk[q] = pack_part(u2f(s[2 * q]), u2f(s[2 * q + 1]), low);
           tmem_st_32x32b_x16(ts, pk);
         }
 #pragma unroll
@@ -671,8 +700,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) e[i] = (vis >> (c + i)) & 1 ? e[i] : 0.f;
             }
-            pk[8 * cc + 2 * q] = pack_bf16x2(e[0], e[1]);
-            pk[8 * cc + 2 * q + 1] = pack_bf16x2(e[2], e[3]);
+            pk[8 * cc + 2 * q] = pack_part(e[0], e[1], low);
+            pk[8 * cc + 2 * q + 1] = pack_part(e[2], e[3], low);
           }
         }
         tmem_st_32x32b_x16(ts + 16, pk);
@@ -686,19 +715,26 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         ++n;
         return true;
       };
-      // visible columns of this thread's 32, as bits
+      // visible columns of this thread's 32, as bits; a query that sees one key has dS = 0
+      // exactly (its tile is never full)
+      const bool lone = kTwice && win == 1 && sink == 0;
       if (it.dkv) {                           // columns: rows of query tile q_tile + t
         const int32_t pos = position();
         int32_t d = pos - (int32_t)a.q_pos0 - it.q_tile * tpt;   // first query that sees the key
-        for (int32_t t = 0; ok && t < nt; ++t, d -= tpt) {
+        for (int32_t t = 0; ok && t < nt; ++t) {
           const int32_t e = d + win;                             // first one past the window
+          const bool at0 = kTwice && c0 == 0 && a.q_pos0 == 0 && it.q_tile + tile_of(t) == 0;
+          const uint32_t alone = lone ? ~0u : at0 ? (1u << a.R) - 1u : 0u;
           ok = tile(std::true_type{},
-                    range_bits(d > tpt ? 128 : d * a.R, pos < sink || e > tpt ? 128 : e * a.R, c0));
+                    range_bits(d > tpt ? 128 : d * a.R, pos < sink || e > tpt ? 128 : e * a.R, c0),
+                    kTwice && (t & 1), alone);
+          if (!kTwice || (t & 1)) d -= tpt;
         }
       } else {                                // columns: keys
         const int32_t pos = position();
         for (int32_t t = 0; ok && t < nt; ++t) {
-          ok = tile(std::false_type{}, win_visible(it.w, 4 * t + wg, pos, sink));   // 32 keys a thread
+          ok = tile(std::false_type{}, win_visible(it.w, 4 * tile_of(t) + wg, pos, sink),
+                    kTwice && (t & 1), lone || pos == 0 ? ~0u : 0u);
         }
       }
       if (!ok) break;
@@ -805,11 +841,13 @@ cudaError_t launch_window_attn_bwd(const CUtensorMap& tm_q, const CUtensorMap& t
                                    const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                    const CUtensorMap& tm_k32, const CUtensorMap& tm_v32,
                                    WindowArgs a, void* ws, cudaStream_t st) {
-  static KernelSetup setup;
-  int sms = 0;
-  cudaError_t e = kernel_setup(setup, reinterpret_cast<const void*>(window_attn_bwd_kernel), kWbSmemBytes, kWbRegsAtLaunch, &sms);
-  if (e != cudaSuccess) return e;
   const WbPlan pl = wb_plan(a);
+  auto kernel = pl.twice ? window_attn_bwd_kernel<true> : window_attn_bwd_kernel<false>;
+  static KernelSetup setup[2];
+  int sms = 0;
+  cudaError_t e = kernel_setup(setup[pl.twice], reinterpret_cast<const void*>(kernel), kWbSmemBytes,
+                               kWbRegsAtLaunch, &sms);
+  if (e != cudaSuccess) return e;
   WindowBwdArgs p;
   p.w = a;
   uint8_t* w = static_cast<uint8_t*>(ws);
@@ -834,7 +872,7 @@ cudaError_t launch_window_attn_bwd(const CUtensorMap& tm_q, const CUtensorMap& t
   window_bwd_prep_kernel<<<(unsigned)((rows + kWbPrepRows - 1) / kWbPrepRows + 1), 256, 0, st>>>(
       a, delta, table, pbase, p.counter, pl.chunk, p.nblk);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  e = launch_dependent(window_attn_bwd_kernel, (unsigned)min64(p.n_all, sms), kWbThreads,
+  e = launch_dependent(kernel, (unsigned)min64(p.n_all, sms), kWbThreads,
                        kWbSmemBytes, st, tm_q, tm_do, tm_k, tm_v, tm_k32, tm_v32, p);
   if (e != cudaSuccess || pl.n_part == 0) return e;
   const int32_t n_c = (int32_t)(pl.c_hi - pl.c_lo);

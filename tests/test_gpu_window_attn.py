@@ -43,6 +43,9 @@ CASES = [
     (2, 300, 700, 400, 8, 1, 150, 97, [700, 433]),
     (1, 5, 40, 10, 4, 1, 1, 3, [13]),
     (2, 260, 600, 300, 16, 1, 33, 129, [560, 301]),
+    (2, 600, 600, 0, 16, 2, 1, 0, None),             # every row sees itself only
+    (1, 1500, 1700, 200, 16, 1, 3, 1, [1650]),
+    (2, 130, 130, 0, 8, 1, 0, 0, [130, 77]),
 ]
 
 
@@ -106,6 +109,36 @@ def test_backward(case):
     pipeline.window_backward(buf, q, k, v, d_o, kv_len)
     for x, y in zip(first, (dq, dk, dv)):
         assert torch.equal(x, y)                      # no order of sums is left to chance
+
+
+@pytest.mark.parametrize("case", [CASES[5], CASES[9][:1] + (40, 45, 5, 16, 2, 0, 0, None),
+                                  (2, 900, 900, 0, 16, 2, 2, 0, None)], ids=str)
+def test_few_terms_keep_one_rounding(case):
+    """Few keys a row, or few tiles: P and dS keep 16 bits, so the gradients are off by their
+    own rounding alone.  It is at most half a step, 2^-8 of a value, spread evenly: 2^-8 /
+    sqrt(3) in the Frobenius norm over thousands of values (5 % for the sample), and 2^-14
+    for P, dS and D.  (With P and dS in 8 bits: 2^-8 sqrt(2 / 3), less the values' spread.)"""
+    B, n_q, n_kv, pos0, H, G, W, S, lens = case
+    q, k, v, d_o, _ = _inputs(case)
+    buf = pipeline.WindowBuffers.allocate(pipeline.window_dims(B, n_q, n_kv, pos0, H, G), W, S,
+                                          backward=True)
+    pipeline.window_forward(buf, q, k, v)
+    grads = pipeline.window_backward(buf, q, k, v, d_o)
+    for b, o, l, _, want in _expect(case, q, k, v, d_o, 1 / math.sqrt(128)):
+        for x, (e, _) in zip(grads, want):
+            assert float((x[b].double() - e).norm() / e.norm()) <= 1.05 * 2 ** -8 / 3 ** 0.5 + 2 ** -14
+
+
+def test_a_row_that_sees_one_key_has_no_gradient():
+    for case in ((2, 1, 1, 0, 8, 2, 0, 0, None), (1, 700, 900, 100, 16, 4, 1, 0, None)):
+        B, n_q, n_kv, pos0, H, G, W, S, lens = case
+        q, k, v, d_o, _ = _inputs(case)
+        buf = pipeline.WindowBuffers.allocate(pipeline.window_dims(B, n_q, n_kv, pos0, H, G), W, S,
+                                              backward=True)
+        pipeline.window_forward(buf, q, k, v)
+        dq, dk, dv = pipeline.window_backward(buf, q, k, v, d_o)
+        assert torch.count_nonzero(dq) == 0 and torch.count_nonzero(dk) == 0
+        assert torch.count_nonzero(dv[:, :, pos0:pos0 + n_q]) > 0
 
 
 def test_backward_without_the_kept_bits():
