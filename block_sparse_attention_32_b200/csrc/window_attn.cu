@@ -20,6 +20,10 @@
 // when that would leave SMs without work, one row tile whose key tiles the halves
 // take in turn, each with its own (m, l, O), joined at the end.  Key tiles start
 // at the first key the item's window reaches (TMA rows need no alignment).
+// Few row tiles of many keys: a cluster of up to 8 CTAs takes one row tile, each a run of
+// its key tiles; their (m, l, O) meet through distributed shared memory, every CTA joining
+// and storing a slice of the rows (16 queries over 32768 keys, 16 / 2 heads: 45 us, one CTA
+// a tile 227).
 // TMEM: one S buffer (128 columns) that the halves use in turn, P_A, P_B (64 each),
 // O_A, O_B (128 each).  S is free again as soon as it is in registers, so neither
 // half waits for a product of its own: the next S is made while a half is at its
@@ -66,6 +70,7 @@ enum {
 constexpr int kWaOffMisc = kWaOffBar + WB_COUNT * 8;
 constexpr int kWaOffItem = kWaOffMisc + 16;              // two slots
 constexpr int kWaSmemBytes = 1024 + kWaOffItem + 2 * (int)sizeof(WinItem);
+constexpr int kWaMaxCluster = 8;                        // the portable limit
 constexpr int kWaItemReaders = 10;                      // warps 0-7, 9, 10
 static_assert(kWaSmemBytes <= 232448, "shared memory per block");
 // the 8 bits of x behind its bf16 rounding b (as fp32 bits): a signed count of 2^8
@@ -82,9 +87,38 @@ __device__ __forceinline__ void st_words_v8(void* p, const uint32_t* w) {
   st_global_v8(static_cast<float*>(p), u2f(w[0]), u2f(w[1]), u2f(w[2]), u2f(w[3]), u2f(w[4]),
                u2f(w[5]), u2f(w[6]), u2f(w[7]));
 }
+// O of a CTA's share for the join: rows of 132 floats (16-byte stores of 8 lanes meet no bank twice)
+constexpr int kWaJoinRow = 132;
+static_assert(128 * kWaJoinRow * 4 <= kWaRing * 32768, "the join's rows lie in the ring");
+__device__ __forceinline__ uint32_t peer_smem(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_peer_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_peer_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+// all threads of all CTAs of the cluster; every path of the kernel comes here
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile(
+      "barrier.cluster.arrive.release;\n\t"
+      "barrier.cluster.wait.acquire;" ::: "memory");
+}
 constexpr float kLazyLog2 = 8.f;     // rescale O when a row's maximum grows by more than 2^8
 }  // namespace
 
+// kCluster: launched in clusters of n_share CTAs (else n_share is 1)
+template <bool kCluster>
 __global__ void __launch_bounds__(kWaThreads, 1)
     window_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                            const __grid_constant__ CUtensorMap tm_k,
@@ -92,7 +126,8 @@ __global__ void __launch_bounds__(kWaThreads, 1)
                            const __grid_constant__ CUtensorMap tm_k32,
                            const __grid_constant__ CUtensorMap tm_v32,
                            const __grid_constant__ WindowArgs a, int32_t tiles_per_item,
-                           int32_t n_items) {
+                           int32_t n_items, int32_t n_share) {
+  const int32_t cluster = kCluster ? n_share : 1;
   extern __shared__ uint8_t smem_raw[];
   // (an offset, so that the compiler still knows the address space)
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -110,7 +145,12 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       prefetch_tensormap(&tm_k);
       prefetch_tensormap(&tm_v);
     }
-    win_item(it0, a, (int32_t)blockIdx.x, tiles_per_item);
+    win_item(it0, a, (int32_t)(blockIdx.x / (uint32_t)cluster), tiles_per_item);
+    if (kCluster) {                       // this CTA's run of the key tiles
+      const int32_t r = (int32_t)(blockIdx.x % (uint32_t)cluster), nt = it0.nt;
+      it0.j0 = nt * r / cluster;
+      it0.nt = nt * (r + 1) / cluster - it0.j0;
+    }
   }
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
@@ -191,7 +231,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       if (lane == 0) {
         uint8_t* dst = base + kWaOffRing + s * 32768;
         mbar_arrive_expect_tx(bar + WB_KV_FULL + s, 32768u);
-        win_load_keys(dst, tm, tm32, bar + WB_KV_FULL + s, it, j);
+        win_load_keys(dst, tm, tm32, bar + WB_KV_FULL + s, it, it.j0 + j);
       }
       ++n;
       return true;
@@ -201,7 +241,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       const uint32_t at = (k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
       const int64_t i = (int64_t)k * gridDim.x + at;
       if (k >= 2 && !W(WB_ITEM_EMPTY + (int)(k & 1), (k >> 1) - 1)) break;
-      const bool end = i >= n_items;
+      const bool end = kCluster ? k > 0 : i >= n_items;
       if (k > 0 && !end) win_item(it, a, (int32_t)i, tiles_per_item);
       if (lane == 0) {
         *item_slot(k) = it;
@@ -307,7 +347,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           if (!W(WB_KV_FULL + slot, sv / kWaRing)) { ok = false; return; }
           // keys past the sequence's end may hold anything: their V rows are cleared
           // (P is 0 there, and 0 * NaN would not be)
-          if (a.kv_len != nullptr && cur->len < a.n_kv) win_clear_keys(tile, *cur, j, lane);
+          if (a.kv_len != nullptr && cur->len < a.n_kv) win_clear_keys(tile, *cur, cur->j0 + j, lane);
         }
         if (!begun[x] && no[x] > 0 && !W(WB_O_EMPTY + x, no[x] - 1)) { ok = false; return; }
         if (!W(WB_P_FULL + x, np[x])) { ok = false; return; }
@@ -365,7 +405,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       const int n_st = n_steps();
       for (int k = x; k < n_st; k += 2) {
         if (!takes(k)) continue;
-        const int j = tile_of(k);
+        const int j = it.j0 + tile_of(k);
         if (!W(WB_S_FULL + x, ns)) { ok = false; break; }
         ++ns;
         tc_fence_after();
@@ -477,8 +517,32 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         fb = ex2_approx(mb.x - z);
         l = ma.y * fa + mb.y * fb;
       }
-      // the item's rows leave: o = O / l
       const bool has = split ? it.nt > 0 : begun, both = split && it.nt > 1;
+      if (kCluster) {                     // to shared memory, for the join below
+        float* orow = reinterpret_cast<float*>(base + kWaOffRing) + row * kWaJoinRow;
+        if (x == 0) ml[256 + row] = make_float2(m, l);
+#pragma unroll 1
+        for (int cc = 4 * x; cc < 4 * x + 4; ++cc) {
+          uint32_t r[16], rb[16];
+          if (has) tmem_ld_32x32b_x16(lanes + kColO + 16 * cc, r);
+          if (both) tmem_ld_32x32b_x16(lanes + kColO + 128 + 16 * cc, rb);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            float u = has ? u2f(r[q]) * fa : 0.f;
+            if (both) u += u2f(rb[q]) * fb;
+            r[q] = f2u(u);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(orow + 16 * cc + 4 * q) =
+                make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+        }
+        tc_fence_before();
+        done_item(ki);
+        continue;
+      }
+      // the item's rows leave: o = O / l
       const bool store = i_row < a.n_q;
       const bool live = store && t < it.len && has;
       const int64_t orow =
@@ -539,6 +603,53 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       done_item(ki);
     }
   }
+  if (kCluster) {
+    // the shares' (m, l, O) of each row, in the CTAs' order: a slice of the rows per CTA
+    cluster_sync();
+    if (warp < 8) {
+      const WinItem& it = *item_slot(0);
+      const uint32_t rank = blockIdx.x % (uint32_t)cluster;
+      const int rows = 128 / cluster;
+      for (int u = tid; u < rows * 16; u += 256) {
+        const int row = (int)rank * rows + (u >> 4), col = 8 * (u & 15);
+        const int32_t i_row = it.i0 + row / a.R;
+        const float2* mlc = reinterpret_cast<const float2*>(base + kWaOffML) + 256 + row;
+        const float* oc =
+            reinterpret_cast<const float*>(base + kWaOffRing) + row * kWaJoinRow + col;
+        float mx = -INFINITY;
+        for (int c = 0; c < cluster; ++c) mx = fmaxf(mx, ld_peer_f2(peer_smem(mlc, c)).x);
+        const float z = mx == -INFINITY ? 0.f : mx;
+        float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < cluster; ++c) {
+          const float2 v = ld_peer_f2(peer_smem(mlc, c));
+          const uint32_t src = peer_smem(oc, c);
+          const float4 p = ld_peer_f4(src), q = ld_peer_f4(src + 16);
+          const float f = ex2_approx(v.x - z);
+          l += f * v.y;
+          o[0] += f * p.x; o[1] += f * p.y; o[2] += f * p.z; o[3] += f * p.w;
+          o[4] += f * q.x; o[5] += f * q.y; o[6] += f * q.z; o[7] += f * q.w;
+        }
+        if (i_row >= a.n_q) continue;
+        const bool live = it.q_pos0 + i_row < it.len && l != 0.f;
+        const float inv = live ? 1.f / l : 0.f;
+        const int64_t orow = ((int64_t)it.b * a.n_q + i_row) * ((int64_t)a.G * a.R) +
+                             (int64_t)it.g * a.R + row % a.R;
+        uint32_t pk[4];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) o[q] = live ? o[q] * inv : 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) pk[q] = pack_bf16x2(o[2 * q], o[2 * q + 1]);
+        *reinterpret_cast<uint4*>(a.out + orow * kHeadDim + col) =
+            make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        if (a.rest != nullptr)
+          *reinterpret_cast<uint2*>(a.rest + orow * kHeadDim + col) =
+              make_uint2(rest_pair(o[0], o[1], pk[0], rest_pair(o[2], o[3], pk[1], 0u)),
+                         rest_pair(o[4], o[5], pk[2], rest_pair(o[6], o[7], pk[3], 0u)));
+        if (col == 0) a.lse[orow] = live ? mx * 0.6931471805599453f + logf(l) : -INFINITY;
+      }
+    }
+    cluster_sync();                          // nobody's shared memory goes before it was read
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -549,9 +660,10 @@ cudaError_t launch_window_attn_fwd(const CUtensorMap& tm_q, const CUtensorMap& t
                                    const CUtensorMap& tm_v, const CUtensorMap& tm_k32,
                                    const CUtensorMap& tm_v32, const WindowArgs& a,
                                    cudaStream_t st) {
-  static KernelSetup setup;
+  static KernelSetup setup[2];
   int sms = 0;
-  cudaError_t e = kernel_setup(setup, reinterpret_cast<const void*>(window_attn_fwd_kernel), kWaSmemBytes, kWaRegsAtLaunch, &sms);
+  cudaError_t e = kernel_setup(setup[0], reinterpret_cast<const void*>(window_attn_fwd_kernel<false>),
+                               kWaSmemBytes, kWaRegsAtLaunch, &sms);
   if (e != cudaSuccess) return e;
   // two row tiles per item share the key tiles' loads (8192 tokens, 64 heads: 274 us, one
   // per item 373); one per item when all of them run at once (1024 tokens, 16 heads: 16.4
@@ -560,8 +672,38 @@ cudaError_t launch_window_attn_fwd(const CUtensorMap& tm_q, const CUtensorMap& t
   const int32_t per = a.batch * a.G * tiles <= sms ? 1 : 2;
   const int64_t items = a.batch * a.G * ((tiles + per - 1) / per);
   if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  window_attn_fwd_kernel<<<(unsigned)min64(items, sms), kWaThreads, kWaSmemBytes, st>>>(
-      tm_q, tm_k, tm_v, tm_k32, tm_v32, a, per, (int32_t)items);
+  // keys of the longest row tile.  The join costs 2 us: two CTAs a tile from 2048 keys on
+  // (there 24.6 us either way; 1024 keys: 18.4, alone 16.4), four from 4096 (512 queries, 8 / 1
+  // heads: 24.6, alone 36.9), eight from 8192 and only while all clusters run at once:
+  // sixteen of eight did not (36.9 us, in fours 22.6)
+  int64_t keys = a.q_pos0 + a.n_q;
+  if (a.window > 0) keys = min64(keys, min64(a.window, keys) + 128 / a.R + a.sink);
+  int cluster = 1;
+  while (per == 1 && cluster < kWaMaxCluster && keys >= 2048 * cluster &&
+         items * 2 * cluster <= (cluster < 4 ? sms * 7 / 8 : sms / 2))
+    cluster *= 2;
+  if (cluster == 1) {
+    window_attn_fwd_kernel<false><<<(unsigned)min64(items, sms), kWaThreads, kWaSmemBytes, st>>>(
+        tm_q, tm_k, tm_v, tm_k32, tm_v32, a, per, (int32_t)items, 1);
+    return cudaGetLastError();
+  }
+  e = kernel_setup(setup[1], reinterpret_cast<const void*>(window_attn_fwd_kernel<true>),
+                   kWaSmemBytes, kWaRegsAtLaunch, &sms);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * cluster));
+  cfg.blockDim = dim3(kWaThreads);
+  cfg.dynamicSmemBytes = kWaSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)cluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, window_attn_fwd_kernel<true>, tm_q, tm_k, tm_v, tm_k32, tm_v32, a,
+                         per, (int32_t)items, (int32_t)cluster);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 

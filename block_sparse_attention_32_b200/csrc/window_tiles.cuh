@@ -29,6 +29,7 @@ struct WinItem {
   int32_t b, g, i0;          // first query of row tile A
   int32_t q_pos0, W, len;    // len: min(kv_len[b], n_kv)
   int32_t wlo, s_end, nc, nt;
+  int32_t j0;                // first tile of this CTA's share (cluster), its nt tiles follow
   int32_t end_a, beg_b;      // last key tile that A sees; first behind the sinks that B sees
   bool rows[2];              // row tile X has a query below n_q and len
   int32_t x0[2], x1[2];      // positions of its first and last such query
@@ -69,6 +70,7 @@ __device__ __forceinline__ void win_item(WinItem& it, const WindowArgs& a, int32
   it.wlo = max(0, tlo - it.W + 1);
   if (a.sink >= it.wlo) it.wlo = 0;
   it.s_end = (int32_t)min64(a.sink, it.wlo);
+  it.j0 = 0;
   it.nc = thi < 0 ? 0 : (it.s_end + 31) / 32;
   it.nt = thi < 0 ? 0 : (it.nc + (thi + 1 - it.wlo + 31) / 32 + 3) / 4;
   it.end_a = it.rows[0] ? (it.nc + (it.x1[0] - it.wlo) / 32) / 4 : -1;

@@ -46,6 +46,12 @@ CASES = [
     (2, 600, 600, 0, 16, 2, 1, 0, None),             # every row sees itself only
     (1, 1500, 1700, 200, 16, 1, 3, 1, [1650]),
     (2, 130, 130, 0, 8, 1, 0, 0, [130, 77]),
+    # few rows of many keys: the row tiles are shared by two, four, eight CTAs
+    (1, 16, 2500, 2400, 16, 2, 0, 0, None),
+    (2, 40, 6000, 5900, 16, 2, 0, 0, [5930, 100]),
+    (1, 33, 5000, 4900, 8, 1, 4500, 70, None),
+    (1, 20, 9000, 8900, 8, 1, 0, 0, [8911]),
+    (1, 300, 8700, 8400, 1, 1, 0, 0, None),
 ]
 
 
