@@ -130,8 +130,11 @@ WbPlan wb_plan(const WindowArgs& a) {
   // what the rounding of P and dS left (2^-17 remains).  A training step of 3 x 97 tokens,
   // 8 / 1 heads, L2 cold: 48 us, once 44; 8192 tokens, 32 / 4 heads, window 8: 286 and 220,
   // so not there.
-  p.twice = total <= kWbTwiceTiles ||
-            (a.window > 0 && min64(a.window, a.n_kv) + a.sink <= kWbTwiceKeys);
+  // Not where a dq item walks many key tiles by itself (one query over 4096 keys, 8 / 1
+  // heads: 137 us, once 80).
+  int64_t keys = a.q_pos0 + a.n_q;
+  if (a.window > 0) keys = min64(keys, min64(a.window, keys) + a.sink);
+  p.twice = (total <= kWbTwiceTiles && keys <= 1024) || keys <= kWbTwiceKeys;
   // Tiles of a chunk: few while SMs stand idle (512 tokens, 8 / 1 heads, no window: 4 tiles
   // 46 us, 8: 52, 32: 83), then about 1.6 chunks an SM (1024 tokens, 16 / 2 heads: 62 us, with
   // one an SM 69, with 32 tiles 97; 3 ragged x 1111: 109, with two an SM 115), up to 32 tiles
