@@ -59,7 +59,7 @@ static_assert(kWaRegsControl + 2 * kWaRegsSoftmax == 3 * kWaRegsAtLaunch,
 constexpr int kWaRing = 5;                              // 32 KB K or V tiles in flight
 constexpr int kWaOffQ = 0;                              // Q_A, Q_B
 constexpr int kWaOffRing = 65536;
-constexpr int kWaOffML = 32768;      // m, l of both halves' rows when they share a tile (Q_B is unused)
+constexpr int kWaOffML = 32768;      // m, l of both halves' rows when they share a tile (no Q_B then)
 constexpr int kWaOffBar = kWaOffRing + kWaRing * 32768;
 enum {
   WB_Q_FULL = 0, WB_Q_EMPTY = 2, WB_S_FULL = 4, WB_P_FULL = 6, WB_PV_DONE = 8, WB_O_EMPTY = 10,
@@ -87,7 +87,8 @@ __device__ __forceinline__ void st_words_v8(void* p, const uint32_t* w) {
   st_global_v8(static_cast<float*>(p), u2f(w[0]), u2f(w[1]), u2f(w[2]), u2f(w[3]), u2f(w[4]),
                u2f(w[5]), u2f(w[6]), u2f(w[7]));
 }
-// O of a CTA's share for the join: rows of 132 floats (16-byte stores of 8 lanes meet no bank twice)
+// O of a CTA's share for the join: rows of 132 floats, so that the 16-byte stores of 8
+// lanes meet no bank twice
 constexpr int kWaJoinRow = 132;
 static_assert(128 * kWaJoinRow * 4 <= kWaRing * 32768, "the join's rows lie in the ring");
 __device__ __forceinline__ uint32_t peer_smem(const void* p, uint32_t rank) {
@@ -105,7 +106,10 @@ __device__ __forceinline__ float4 ld_peer_f4(uint32_t a) {
 }
 __device__ __forceinline__ float2 ld_peer_f2(uint32_t a) {
   float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(a)
+               : "memory");
   return v;
 }
 // all threads of all CTAs of the cluster; every path of the kernel comes here
@@ -347,7 +351,8 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           if (!W(WB_KV_FULL + slot, sv / kWaRing)) { ok = false; return; }
           // keys past the sequence's end may hold anything: their V rows are cleared
           // (P is 0 there, and 0 * NaN would not be)
-          if (a.kv_len != nullptr && cur->len < a.n_kv) win_clear_keys(tile, *cur, cur->j0 + j, lane);
+          if (a.kv_len != nullptr && cur->len < a.n_kv)
+            win_clear_keys(tile, *cur, cur->j0 + j, lane);
         }
         if (!begun[x] && no[x] > 0 && !W(WB_O_EMPTY + x, no[x] - 1)) { ok = false; return; }
         if (!W(WB_P_FULL + x, np[x])) { ok = false; return; }
@@ -585,8 +590,9 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           if (a.rest != nullptr) {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              rest[q] = rest_pair(u2f(r[4 * q]), u2f(r[4 * q + 1]), pk[2 * q],
-                                  rest_pair(u2f(r[4 * q + 2]), u2f(r[4 * q + 3]), pk[2 * q + 1], 0u));
+              rest[q] = rest_pair(
+                  u2f(r[4 * q]), u2f(r[4 * q + 1]), pk[2 * q],
+                  rest_pair(u2f(r[4 * q + 2]), u2f(r[4 * q + 3]), pk[2 * q + 1], 0u));
             uint4* ro = reinterpret_cast<uint4*>(a.rest + orow * kHeadDim + 32 * cc);
             ro[0] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
             ro[1] = make_uint4(rest[4], rest[5], rest[6], rest[7]);
@@ -662,8 +668,9 @@ cudaError_t launch_window_attn_fwd(const CUtensorMap& tm_q, const CUtensorMap& t
                                    cudaStream_t st) {
   static KernelSetup setup[2];
   int sms = 0;
-  cudaError_t e = kernel_setup(setup[0], reinterpret_cast<const void*>(window_attn_fwd_kernel<false>),
-                               kWaSmemBytes, kWaRegsAtLaunch, &sms);
+  cudaError_t e =
+      kernel_setup(setup[0], reinterpret_cast<const void*>(window_attn_fwd_kernel<false>),
+                   kWaSmemBytes, kWaRegsAtLaunch, &sms);
   if (e != cudaSuccess) return e;
   // two row tiles per item share the key tiles' loads (8192 tokens, 64 heads: 274 us, one
   // per item 373); one per item when all of them run at once (1024 tokens, 16 heads: 16.4

@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       }
       __syncwarp();
     } else {
-      // ---------------- -lse log2 e, -D of the streamed rows (dk, dv) or the item's (dq) ----------------
+      // ------------ -lse log2 e, -D of the streamed rows (dk, dv) or the item's (dq) ------------
       grid_wait();                           // and so is D
       uint32_t n = 0;                        // slots filled: one per tile, or per dq item
       bool ok = true;

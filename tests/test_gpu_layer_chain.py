@@ -175,11 +175,18 @@ def _decode(seed, B=5, H=32, G=4):
     return (lambda: pipeline.paged_decode(buf, q, cache)), [buf.out, buf.lse, buf.dev_err]
 
 
+def _chunk(seed, n=24, n_kv=5000, H=16, G=2):
+    """A few queries over a long context: CTAs share a row tile."""
+    q, k, v = _rn(seed, 1, n, H, 128), _rn(seed + 1, 1, G, n_kv, 128), _rn(seed + 2, 1, G, n_kv, 128)
+    win = pipeline.WindowBuffers.allocate(pipeline.window_dims(1, n, n_kv, n_kv - n, H, G))
+    return (lambda: pipeline.window_forward(win, q, k, v)), [win.out, win.lse, win.dev_err]
+
+
 @pytest.mark.parametrize("captured", [False, True])
 def test_steps_side_by_side_on_streams(captured):
-    """Two training steps and two decode steps, each with buffers of its own, run over
-    each other on four streams, eagerly or as replayed graphs: the bits of a lone run."""
-    jobs = [_step(10), _decode(20), _step(30), _decode(40)]
+    """Training steps, decode steps and a chunk, each with buffers of its own, run over each
+    other on five streams, eagerly or as replayed graphs: the bits of a lone run."""
+    jobs = [_step(10), _decode(20), _step(30), _chunk(50), _decode(40)]
     alone = []
     for run, outs in jobs:
         run()
