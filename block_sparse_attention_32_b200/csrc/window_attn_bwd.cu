@@ -36,7 +36,8 @@
 // Where few keys a row or few tiles are at stake, every tile comes twice, for the high and
 // the low parts of P and dS (wb_plan).
 // A key block that many queries see (sinks; no window) is cut into chunks of
-// query tiles whose fp32 sums a last kernel adds in chunk order.
+// query tiles whose fp32 sums a last kernel adds in chunk order; few row tiles of many
+// keys share those among several dq items, added the same way.
 // Measured: 8192 tokens, 64 / 8 heads, W = 1024, S = 4: 860 us (0.905 TFLOP of visible
 // pairs' products: 1.05 PFLOP/s, 0.64 of the burst rate) + 50 for D and the work list.
 // The tensor pipe is busy 0.55 of its cycles.  With the softmax taken out (timed, wrong
@@ -89,7 +90,8 @@ struct WindowBwdArgs {
   const int32_t* pbase;     // [nblk]: first partial of a cut block, -1 for an uncut one
   int32_t* counter;
   float* part;              // [B * G, n_part, 2, 128, 128]: dV, dK sums of a chunk
-  int32_t chunk, nblk, n_cut, n_part, n_dkv, n_all;
+  float* part_q;            // [n_dq, kq, 128, 128]: dQ sums of a row tile's shares of its keys
+  int32_t chunk, nblk, n_cut, n_part, n_dkv, n_all, kq;
 };
 
 // query tiles (128 / R tokens) that see key block c: [first, first + count)
@@ -111,7 +113,7 @@ constexpr int64_t kWbTwiceTiles = 64, kWbTwiceKeys = 4;   // query x key tiles; 
 
 struct WbPlan {
   int64_t nblk, n_cut, n_part, c_lo, c_hi, n_dkv, n_dq;   // c_lo .. c_hi: the cut blocks' range
-  int32_t chunk;
+  int32_t chunk, kq;         // kq: items that share a row tile's keys
   bool twice;
 };
 WbPlan wb_plan(const WindowArgs& a) {
@@ -130,8 +132,8 @@ WbPlan wb_plan(const WindowArgs& a) {
   // what the rounding of P and dS left (2^-17 remains).  A training step of 3 x 97 tokens,
   // 8 / 1 heads, L2 cold: 48 us, once 44; 8192 tokens, 32 / 4 heads, window 8: 286 and 220,
   // so not there.
-  // Not where a dq item walks many key tiles by itself (one query over 4096 keys, 8 / 1
-  // heads: 137 us, once 80).
+  // Not where dq items walk many key tiles (one query over 4096 keys, 8 / 1 heads, in one
+  // item: 137 us, once 80).
   int64_t keys = a.q_pos0 + a.n_q;
   if (a.window > 0) keys = min64(keys, min64(a.window, keys) + a.sink);
   p.twice = (total <= kWbTwiceTiles && keys <= 1024) || keys <= kWbTwiceKeys;
@@ -154,6 +156,11 @@ WbPlan wb_plan(const WindowArgs& a) {
   }
   p.n_dkv = p.n_cut * a.batch * a.G;
   p.n_dq = a.batch * a.G * ((a.n_q * a.R + 127) / 128);
+  // few row tiles of many keys: up to eight items a tile, four key tiles each at least (a
+  // training step of one query over 4096 keys, 8 / 1 heads, L2 cold: 49 us, 78 in one; 16 over
+  // 32768, 16 / 2 heads: 125 and 385; 16 over 1024: 59 and 65)
+  p.kq = 1;
+  while (p.kq < 8 && p.n_dq * p.kq * 2 <= 148 && keys >= 1024 * p.kq) p.kq *= 2;
   return p;
 }
 size_t pad32(size_t n) { return (n + 31) / 32 * 32; }
@@ -191,7 +198,11 @@ __device__ __forceinline__ void wb_item(WbItem& it, const WindowBwdArgs& p, int3
     const int32_t end = live <= 0 || it.k0 >= it.len ? 0 : (int32_t)((live + tpt - 1) / tpt);
     it.nt = max(0, min(q1 - q0, end - it.q_tile));
   } else {
-    win_item(it.w, a, idx - p.n_dkv, 1);
+    const int32_t e = idx - p.n_dkv, tile = e / p.kq, c = e - tile * p.kq;
+    win_item(it.w, a, tile, 1);
+    it.part = p.kq > 1 ? e : -1;
+    it.w.j0 = it.w.nt * c / p.kq;
+    it.w.nt = it.w.nt * (c + 1) / p.kq - it.w.j0;
     it.b = it.w.b;
     it.g = it.w.g;
     it.nt = it.w.nt;
@@ -426,7 +437,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
                      (it.q_tile + tile_of(t)) * tpt);
               else
                 win_load_keys(dst, h ? &tm_v : &tm_k, h ? &tm_v32 : &tm_k32,
-                              bar + XB_STR_FULL + s, it.w, tile_of(t));
+                              bar + XB_STR_FULL + s, it.w, it.w.j0 + tile_of(t));
             }
             if (ok) issued[h] = n + 1;
           }
@@ -469,7 +480,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
                            (it.len - (int32_t)a.q_pos0 - (it.q_tile + tile_of(t)) * tpt) * a.R, 128,
                            lane);
           else
-            win_clear_keys(rows, it.w, tile_of(t), lane);
+            win_clear_keys(rows, it.w, it.w.j0 + tile_of(t), lane);
         }
         return true;
       };
@@ -736,7 +747,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       } else {                                // columns: keys
         const int32_t pos = position();
         for (int32_t t = 0; ok && t < nt; ++t) {
-          ok = tile(std::false_type{}, win_visible(it.w, 4 * tile_of(t) + wg, pos, sink),
+          ok = tile(std::false_type{}, win_visible(it.w, 4 * (it.w.j0 + tile_of(t)) + wg, pos, sink),
                     kTwice && (t & 1), lone || pos == 0 ? ~0u : 0u);
         }
       }
@@ -754,11 +765,12 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       const int32_t pos = position();
       const bool store = it.dkv ? pos < a.n_kv : query() < a.n_q;
       const bool live = any && store && pos < it.len;
-      const bool part = it.dkv && it.part >= 0;
+      const bool part = it.part >= 0;
       uint8_t* dst;
       if (part)
         dst = reinterpret_cast<uint8_t*>(
-            p.part + (((int64_t)it.part * 2 + which) * 128 + row) * kHeadDim + oc);
+            it.dkv ? p.part + (((int64_t)it.part * 2 + which) * 128 + row) * kHeadDim + oc
+                   : p.part_q + ((int64_t)it.part * 128 + row) * kHeadDim + oc);
       else if (it.dkv)
         dst = reinterpret_cast<uint8_t*>(
             (which == 0 ? a.dv : a.dk) +
@@ -832,12 +844,40 @@ __global__ void __launch_bounds__(256)
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
 }
 
+// dq of row tiles whose keys were shared: the shares' sums in their order, 4 values a thread.
+// Row tiles count down from the last queries, as items do.
+__global__ void __launch_bounds__(256)
+    window_bwd_join_dq_kernel(const __grid_constant__ WindowBwdArgs p) {
+  grid_wait();
+  const WindowArgs& a = p.w;
+  const int32_t tile = blockIdx.x, i = blockIdx.y * 256 + threadIdx.x;   // of 128 x 32 float4
+  const int32_t n_bg = (int32_t)a.batch * a.G, tpt = 128 / a.R;
+  const int32_t n_it = ((int32_t)a.n_q + tpt - 1) / tpt, r = tile / n_bg, bg = tile - r * n_bg;
+  const float4* src = reinterpret_cast<const float4*>(p.part_q) + (int64_t)tile * p.kq * 4096 + i;
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int32_t j = 0; j < p.kq; ++j) {
+    const float4 u = __ldg(src + (int64_t)j * 4096);
+    t.x += u.x;
+    t.y += u.y;
+    t.z += u.z;
+    t.w += u.w;
+  }
+  const int32_t row = i >> 5, b = bg / a.G, g = bg - b * a.G;
+  const int64_t q = (int64_t)(n_it - 1 - r) * tpt + row / a.R;
+  if (q >= a.n_q) return;
+  __nv_bfloat16* dst = a.dq + (((int64_t)b * a.n_q + q) * a.G * a.R + (int64_t)g * a.R + row % a.R) *
+                                  kHeadDim + 4 * (i & 31);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+}
+
 size_t window_attn_bwd_workspace(const WindowArgs& a) {
   const WbPlan p = wb_plan(a);
-  if (p.n_dkv + p.n_dq > 0x7FFFFF00 || a.batch * a.n_q * a.G * a.R > 0x7FFFFF00) return 0;
+  if (p.n_dkv + p.n_dq * p.kq > 0x7FFFFF00 || a.batch * a.n_q * a.G * a.R > 0x7FFFFF00) return 0;
   return pad32((size_t)a.batch * a.n_q * a.G * a.R * 4) + pad32((size_t)p.n_cut * 8) +
          pad32((size_t)p.nblk * 4) + 32 +
-         (size_t)a.batch * a.G * p.n_part * 2 * 128 * 128 * sizeof(float);
+         ((size_t)a.batch * a.G * p.n_part * 2 + (p.kq > 1 ? p.n_dq * p.kq : 0)) * 128 * 128 *
+             sizeof(float);
 }
 
 cudaError_t launch_window_attn_bwd(const CUtensorMap& tm_q, const CUtensorMap& tm_do,
@@ -870,17 +910,23 @@ cudaError_t launch_window_attn_bwd(const CUtensorMap& tm_q, const CUtensorMap& t
   p.n_cut = (int32_t)pl.n_cut;
   p.n_part = (int32_t)pl.n_part;
   p.n_dkv = (int32_t)pl.n_dkv;
-  p.n_all = (int32_t)(pl.n_dkv + pl.n_dq);
+  p.n_all = (int32_t)(pl.n_dkv + pl.n_dq * pl.kq);
+  p.part_q = p.part + (size_t)a.batch * a.G * pl.n_part * 2 * 128 * 128;
+  p.kq = pl.kq;
   const int64_t rows = a.batch * a.n_q * a.G * a.R;
   window_bwd_prep_kernel<<<(unsigned)((rows + kWbPrepRows - 1) / kWbPrepRows + 1), 256, 0, st>>>(
       a, delta, table, pbase, p.counter, pl.chunk, p.nblk);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_dependent(kernel, (unsigned)min64(p.n_all, sms), kWbThreads,
                        kWbSmemBytes, st, tm_q, tm_do, tm_k, tm_v, tm_k32, tm_v32, p);
-  if (e != cudaSuccess || pl.n_part == 0) return e;
-  const int32_t n_c = (int32_t)(pl.c_hi - pl.c_lo);
-  return launch_dependent(window_bwd_join_kernel, dim3((unsigned)(a.batch * a.G * n_c), 32), 256, 0,
-                          st, p, (int32_t)pl.c_lo, n_c);
+  if (e == cudaSuccess && pl.n_part > 0) {
+    const int32_t n_c = (int32_t)(pl.c_hi - pl.c_lo);
+    e = launch_dependent(window_bwd_join_kernel, dim3((unsigned)(a.batch * a.G * n_c), 32), 256, 0,
+                         st, p, (int32_t)pl.c_lo, n_c);
+  }
+  if (e == cudaSuccess && pl.kq > 1)
+    e = launch_dependent(window_bwd_join_dq_kernel, dim3((unsigned)pl.n_dq, 16), 256, 0, st, p);
+  return e;
 }
 
 }  // namespace msa
