@@ -33,8 +33,8 @@
 // wait for dV(n): 4300 clocks a tile.)  Per tile: dP(n), dK(n-1), dV(n-1), S(n+1).
 // Q and dO (K and V) slots are freed apart: three for the first, which S needs early
 // and dK keeps late, two for the second.
-// Where few keys a row or few tiles are at stake, every tile comes twice, for the high and
-// the low parts of P and dS (wb_plan).
+// Where rows see few keys or sequences are short, tiles come twice, for the high and the
+// low parts of P and dS (wb_plan, wb_item).
 // A key block that many queries see (sinks; no window) is cut into chunks of
 // query tiles whose fp32 sums a last kernel adds in chunk order; few row tiles of many
 // keys share those among several dq items, added the same way.
@@ -109,7 +109,8 @@ __host__ __device__ __forceinline__ int32_t wb_chunks(int32_t count, int32_t chu
   return count <= chunk ? 1 : (count + chunk - 1) / chunk;
 }
 
-constexpr int64_t kWbTwiceTiles = 64, kWbTwiceKeys = 4;   // query x key tiles; keys a row
+constexpr int64_t kWbTwiceKeys = 4;         // keys a row
+constexpr int64_t kWbTwiceTerms = 2048;     // tile pairs of one (batch, group) x keys a row
 
 struct WbPlan {
   int64_t nblk, n_cut, n_part, c_lo, c_hi, n_dkv, n_dq;   // c_lo .. c_hi: the cut blocks' range
@@ -125,18 +126,20 @@ WbPlan wb_plan(const WindowArgs& a) {
     wb_query_tiles(a, c, f, n);
     total += n;
   }
-  total *= a.batch * a.G;
-  // Tiles twice: a sum of few terms keeps the full error of P's and dS's rounding to bf16,
-  // 2^-8 a term, beside the result's own.  Where rows see few keys, or a problem is so small
-  // that launches are its time, each tile comes twice, and the second time the sums take
-  // what the rounding of P and dS left (2^-17 remains).  A training step of 3 x 97 tokens,
-  // 8 / 1 heads, L2 cold: 48 us, once 44; 8192 tokens, 32 / 4 heads, window 8: 286 and 220,
-  // so not there.
-  // Not where dq items walk many key tiles (one query over 4096 keys, 8 / 1 heads, in one
-  // item: 137 us, once 80).
+  // Tiles twice: rounded to bf16, P and dS leave 2^-8 of each term in a gradient, as much as
+  // the result's own rounding does.  Where terms cancel (sum_j dS_ij = 0: few keys a row) or
+  // are few, that is neither small beside the sum nor averaged over many roundings (random
+  // inputs, error over that of 32-bit sums rounded once: 1.43 where terms are many, 1.5 to 1.9
+  // for rows of 2 to 4 keys and for a few tiles).  There each tile comes twice, and the second
+  // time the sums take what the rounding of P and dS left (2^-17 remains).  The rule asks
+  // for the shape of one sequence, not for how many of them, or of groups, a call has: the
+  // same sequence's gradients are as exact in a batch as alone.  A training step of 3 x 97
+  // tokens, 8 / 1 heads, L2 cold: 48 us, once 44; 64 x 97: 95 and 76; 32 x 256, 32 / 4 heads:
+  // 337 and 243, 8192 tokens, 32 / 4 heads, window 8: 286 and 220, so not there.
   int64_t keys = a.q_pos0 + a.n_q;
   if (a.window > 0) keys = min64(keys, min64(a.window, keys) + a.sink);
-  p.twice = (total <= kWbTwiceTiles && keys <= 1024) || keys <= kWbTwiceKeys;
+  p.twice = total * keys <= kWbTwiceTerms || keys <= kWbTwiceKeys;
+  total *= a.batch * a.G;
   // Tiles of a chunk: few while SMs stand idle (512 tokens, 8 / 1 heads, no window: 4 tiles
   // 46 us, 8: 52, 32: 83), then about 1.6 chunks an SM (1024 tokens, 16 / 2 heads: 62 us, with
   // one an SM 69, with 32 tiles 97; 3 ragged x 1111: 109, with two an SM 115), up to 32 tiles
@@ -169,12 +172,14 @@ size_t pad32(size_t n) { return (n + 31) / 32 * 32; }
 // shared memory, so that the softmax warps need not hold it in registers
 struct WbItem {
   bool dkv, end;             // end: there are no more
-  int32_t b, g, nt;          // nt: streamed tiles
+  int32_t b, g, nt;          // nt: steps, a streamed tile each
+  int32_t half;              // 1: tiles come twice, in adjacent steps; else 0
   int32_t k0, q_tile, part;  // dkv: first key, first query tile, partial (-1: final)
   int32_t len;
   WinItem w;                 // dq
 };
 static_assert(sizeof(WbItem) <= kWbItemBytes, "an item's slot");
+template <bool kTwice>
 __device__ __forceinline__ void wb_item(WbItem& it, const WindowBwdArgs& p, int32_t idx) {
   const WindowArgs& a = p.w;
   const int32_t bg_all = (int32_t)a.batch * a.G;
@@ -208,6 +213,10 @@ __device__ __forceinline__ void wb_item(WbItem& it, const WindowBwdArgs& p, int3
     it.nt = it.w.nt;
     it.len = it.w.len;
   }
+  // else it is the row tile whose first rows see at most kWbTwiceKeys keys (dq: one item of
+  // a sequence and group; 8192 tokens, 64 / 8 heads, W = 1024: 1234 us, without 1228)
+  it.half = kTwice || (!it.dkv && it.w.i0 == 0 && a.q_pos0 < kWbTwiceKeys) ? 1 : 0;
+  it.nt <<= it.half;
 }
 
 }  // namespace
@@ -380,7 +389,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
   };
   auto done_item = [&](uint32_t k) { arrive(XB_ITEM_EMPTY + (int)(k & 1)); };
   const int32_t tpt = 128 / a.R;             // tokens per query tile
-  auto tile_of = [](int32_t t) { return kTwice ? t >> 1 : t; };    // of step t
+  // streamed tile of step t
+  auto tile_of = [](const WbItem& it, int32_t t) { return t >> (kTwice ? 1 : it.half); };
   const float log2e = 1.4426950408889634f;
 
   if (warp >= kWbCtl) {
@@ -407,8 +417,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         if (lane == 0) idx = atomicAdd(p.counter, 1);
         idx = __shfl_sync(0xffffffffu, idx, 0);
         it.end = idx >= p.n_all;
-        if (!it.end) wb_item(it, p, idx);
-        if (kTwice) it.nt *= 2;
+        if (!it.end) wb_item<kTwice>(it, p, idx);
         if (lane == 0) {
           item_slot(k) = it;
           mbar_arrive(bar + XB_ITEM_FULL + (int)(k & 1));
@@ -434,10 +443,10 @@ __global__ void __launch_bounds__(kWbThreads, 1)
               uint8_t* dst = base + kWbOffStream + s * 32768;
               if (it.dkv)
                 load(dst, h ? &tm_do : &tm_q, bar + XB_STR_FULL + s, it.g * a.R,
-                     (it.q_tile + tile_of(t)) * tpt);
+                     (it.q_tile + tile_of(it, t)) * tpt);
               else
                 win_load_keys(dst, h ? &tm_v : &tm_k, h ? &tm_v32 : &tm_k32,
-                              bar + XB_STR_FULL + s, it.w, it.w.j0 + tile_of(t));
+                              bar + XB_STR_FULL + s, it.w, it.w.j0 + tile_of(it, t));
             }
             if (ok) issued[h] = n + 1;
           }
@@ -477,10 +486,10 @@ __global__ void __launch_bounds__(kWbThreads, 1)
           uint8_t* rows = base + kWbOffStream + s * 32768;
           if (it.dkv)
             win_clear_rows(rows,
-                           (it.len - (int32_t)a.q_pos0 - (it.q_tile + tile_of(t)) * tpt) * a.R, 128,
-                           lane);
+                           (it.len - (int32_t)a.q_pos0 - (it.q_tile + tile_of(it, t)) * tpt) * a.R,
+                           128, lane);
           else
-            win_clear_keys(rows, it.w, it.w.j0 + tile_of(t), lane);
+            win_clear_keys(rows, it.w, it.w.j0 + tile_of(it, t), lane);
         }
         return true;
       };
@@ -587,7 +596,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const int r = 32 * u + lane;
-            const int64_t i = (int64_t)(q_tile + tile_of(t)) * tpt + r / a.R;
+            const int64_t i = (int64_t)(q_tile + (kTwice ? t >> 1 : t)) * tpt + r / a.R;
             const bool live = i < a.n_q && a.q_pos0 + i < it.len;
             const int64_t row =
                 ((int64_t)it.b * a.n_q + i) * ((int64_t)a.G * a.R) + it.g * a.R + r % a.R;
@@ -639,10 +648,12 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       }
       const int32_t win = a.window > 0 ? (int32_t)min64(a.window, int64_t(1) << 30) : 1 << 30;
       const int32_t sink = (int32_t)a.sink;
-      // one tile; kDkv: lse and D come with the columns, P goes to the tensor core too.
-      // Of its 32 columns of the buffer, P takes the first 16, dS the others
+      // one step; kDkv: lse and D come with the columns, P goes to the tensor core too; kHalf:
+      // the tile may come twice (low: this is the second time); alone: columns or row of a
+      // query that sees one key, dS = 0.  Of its 32 columns of the buffer, P takes the first
+      // 16, dS the others
       auto tile = [&](auto kind, uint32_t vis, bool low, uint32_t alone) {
-        constexpr bool kDkv = decltype(kind)::value;
+        constexpr bool kDkv = decltype(kind)::value, kHalf = kTwice || !kDkv;
         const bool full = __all_sync(0xffffffffu, vis == ~0u);
         const ulonglong2* m = reinterpret_cast<const ulonglong2*>(
             base + kWbOffMeta + (int)(nm % kWbMeta) * 1024 + 4 * c0);
@@ -683,10 +694,11 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         tmem_ld_32x32b_x16(ts, d);
         const uint64_t nd2 = pack_f32x2(__float_as_uint(nd), __float_as_uint(nd));
         tmem_ld_wait();
-        if (kTwice) vis &= ~alone;
+        if (kHalf) vis &= ~alone;
         if (kDkv) {
 #pragma unroll
-          for (int q = 0; q < 16; ++q) pk[q] = pack_part(u2f(s[2 * q]), u2f(s[2 * q + 1]), low);
+          for (int q = 0; q < 16; ++q)
+            pk[q] = pack_part(u2f(s[2 * q]), u2f(s[2 * q + 1]), kHalf && low);
           tmem_st_32x32b_x16(ts, pk);
         }
 #pragma unroll
@@ -714,8 +726,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) e[i] = (vis >> (c + i)) & 1 ? e[i] : 0.f;
             }
-            pk[8 * cc + 2 * q] = pack_part(e[0], e[1], low);
-            pk[8 * cc + 2 * q + 1] = pack_part(e[2], e[3], low);
+            pk[8 * cc + 2 * q] = pack_part(e[0], e[1], kHalf && low);
+            pk[8 * cc + 2 * q + 1] = pack_part(e[2], e[3], kHalf && low);
           }
         }
         tmem_st_32x32b_x16(ts + 16, pk);
@@ -729,15 +741,17 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         ++n;
         return true;
       };
-      // visible columns of this thread's 32, as bits; a query that sees one key has dS = 0
-      // exactly (its tile is never full)
-      const bool lone = kTwice && win == 1 && sink == 0;
+      // visible columns of this thread's 32, as bits.  A query that sees one key -- position 0's,
+      // or all -- has dS = 0 exactly (its tile is never full).  In dk, where a sum over many rows
+      // takes one such row in, what it leaves, 2^-17 of a term, is masked only where tiles come
+      // twice, or below, where nothing else is in the sum
+      const bool lone = kTwice && win == 1 && sink == 0;       // all of them
       if (it.dkv) {                           // columns: rows of query tile q_tile + t
         const int32_t pos = position();
         int32_t d = pos - (int32_t)a.q_pos0 - it.q_tile * tpt;   // first query that sees the key
         for (int32_t t = 0; ok && t < nt; ++t) {
           const int32_t e = d + win;                             // first one past the window
-          const bool at0 = kTwice && c0 == 0 && a.q_pos0 == 0 && it.q_tile + tile_of(t) == 0;
+          const bool at0 = kTwice && c0 == 0 && a.q_pos0 == 0 && it.q_tile + (t >> 1) == 0;
           const uint32_t alone = lone ? ~0u : at0 ? (1u << a.R) - 1u : 0u;
           ok = tile(std::true_type{},
                     range_bits(d > tpt ? 128 : d * a.R, pos < sink || e > tpt ? 128 : e * a.R, c0),
@@ -747,8 +761,9 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       } else {                                // columns: keys
         const int32_t pos = position();
         for (int32_t t = 0; ok && t < nt; ++t) {
-          ok = tile(std::false_type{}, win_visible(it.w, 4 * (it.w.j0 + tile_of(t)) + wg, pos, sink),
-                    kTwice && (t & 1), lone || pos == 0 ? ~0u : 0u);
+          ok = tile(std::false_type{},
+                    win_visible(it.w, 4 * (it.w.j0 + tile_of(it, t)) + wg, pos, sink),
+                    t & it.half, it.half && (lone || pos == 0) ? ~0u : 0u);
         }
       }
       if (!ok) break;
@@ -764,7 +779,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       const float f = it.dkv && which == 0 ? 1.f : a.scale;
       const int32_t pos = position();
       const bool store = it.dkv ? pos < a.n_kv : query() < a.n_q;
-      const bool live = any && store && pos < it.len;
+      const bool live = any && store && pos < it.len &&
+                        !(it.dkv && which == 1 && it.len == 1 && a.q_pos0 == 0);
       const bool part = it.part >= 0;
       uint8_t* dst;
       if (part)
