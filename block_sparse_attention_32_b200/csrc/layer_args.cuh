@@ -38,7 +38,9 @@ inline cudaError_t kernel_setup(KernelSetup& done, const void* kernel, int smem,
 
 // Dependent launches: the kernel's blocks may take their places while the one
 // before it on the stream still runs (after its grid_launch_dependents), and
-// wait there, in grid_wait, until it is complete and its writes are visible.
+// wait there, in grid_wait, until it is complete and its writes are visible -- to plain
+// loads: what that kernel wrote is not read by __ldg or through const __restrict__, which
+// promise data that stays as it is while the kernel runs.
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -572,8 +572,8 @@ __global__ void __launch_bounds__(kNrBwdThreads, 2)
 
 // dw = sum over the blocks' partial rows: 32 columns x 32 row slices a block
 __global__ void __launch_bounds__(1024)
-    norm_rope_dw_kernel(const float* __restrict__ part, int32_t n_blocks, int32_t d,
-                        float* __restrict__ dw_q, float* __restrict__ dw_k) {
+    norm_rope_dw_kernel(const float* part, int32_t n_blocks, int32_t d,
+                        float* dw_q, float* dw_k) {
   __shared__ float red[32][33];
   grid_wait();
   const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;

@@ -188,7 +188,7 @@ __device__ __forceinline__ void wb_item(WbItem& it, const WindowBwdArgs& p, int3
     const int32_t e = idx / bg_all, bg = idx - e * bg_all;
     it.b = bg / a.G;
     it.g = bg - it.b * a.G;
-    const int2 t = __ldg(p.table + e);
+    const int2 t = p.table[e];
     int32_t first, count;
     wb_query_tiles(a, t.x, first, count);
     const int32_t k = wb_chunks(count, p.chunk);
@@ -196,7 +196,7 @@ __device__ __forceinline__ void wb_item(WbItem& it, const WindowBwdArgs& p, int3
     int32_t q1 = (int32_t)((int64_t)count * (t.y + 1) / k);
     it.k0 = t.x * 128;
     it.q_tile = first + q0;
-    it.part = k > 1 ? bg * p.n_part + __ldg(p.pbase + t.x) + t.y : -1;
+    it.part = k > 1 ? bg * p.n_part + p.pbase[t.x] + t.y : -1;
     it.len = win_len(a, it.b);
     const int64_t live = (int64_t)it.len - a.q_pos0;         // queries before the padding
     const int32_t tpt = 128 / a.R;
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
                 ((int64_t)it.b * a.n_q + i) * ((int64_t)a.G * a.R) + it.g * a.R + r % a.R;
             // padding: p = 2^{0 - inf} = 0
             v[u][0] = live ? -log2e * __ldg(a.lse + row) : -INFINITY;
-            v[u][1] = live ? -__ldg(p.delta + row) : 0.f;
+            v[u][1] = live ? -p.delta[row] : 0.f;
           }
           if (n >= kWbMeta && !W(XB_META_EMPTY + s, n / kWbMeta - 1)) { ok = false; break; }
           float* m = reinterpret_cast<float*>(base + kWbOffMeta + s * 1024);
@@ -843,11 +843,11 @@ __global__ void __launch_bounds__(256)
   if (k == 1) return;
   const int i = blockIdx.y * 256 + threadIdx.x;             // of 2 x 128 x 32 float4
   const float4* src = reinterpret_cast<const float4*>(p.part) +
-                      ((int64_t)bg * p.n_part + __ldg(p.pbase + c)) * 8192 + i;
+                      ((int64_t)bg * p.n_part + p.pbase[c]) * 8192 + i;
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int32_t j = 0; j < k; ++j) {
-    const float4 u = __ldg(src + (int64_t)j * 8192);
+    const float4 u = src[(int64_t)j * 8192];
     t.x += u.x;
     t.y += u.y;
     t.z += u.z;
@@ -873,7 +873,7 @@ __global__ void __launch_bounds__(256)
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int32_t j = 0; j < p.kq; ++j) {
-    const float4 u = __ldg(src + (int64_t)j * 4096);
+    const float4 u = src[(int64_t)j * 4096];
     t.x += u.x;
     t.y += u.y;
     t.z += u.z;
