@@ -49,6 +49,14 @@ double number(PyObject* o, const char* name) {
   }
   return v;
 }
+int truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    throw Bad(std::string(name) + ": must be true or false");
+  }
+  return v;
+}
 std::string shape_of(at::IntArrayRef s) {
   std::string r = "(";
   for (size_t i = 0; i < s.size(); ++i) r += (i ? ", " : "") + std::to_string(s[i]);
@@ -148,7 +156,7 @@ struct NormRope {
     d.d = (int32_t)some->size(3);
     d.pos0 = integer(opos0, "pos0");
     d.eps = (float)number(oeps, "eps");
-    d.interleaved = PyObject_IsTrue(ointer) ? 1 : 0;
+    d.interleaved = truth(ointer, "interleaved");
     d.rot = tab == nullptr ? 0 : (int32_t)tab->size(1);
     if (tq != nullptr) {
       d.h_q = (int32_t)(tq->dim() == 4 ? tq->size(2) : 0);

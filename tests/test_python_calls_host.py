@@ -1,0 +1,39 @@
+"""The Python calls of the operators around the sparse path, without a GPU: what is refused
+before anything is enqueued, how their module is loaded, where errors are reported."""
+import pytest
+import torch
+
+from block_sparse_attention_32_b200 import build as msa_build
+from block_sparse_attention_32_b200 import capi, pipeline
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    msa_build.build()
+
+
+def _z(*shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype)
+
+
+class _NoTruth:
+    def __bool__(self):
+        raise KeyError("no truth value")
+
+
+@pytest.mark.parametrize("what", [torch.tensor([1, 0]), _NoTruth()], ids=["tensor", "raises"])
+def test_interleaved_without_a_truth_value_is_refused(what):
+    """Refused as the other arguments are, before the tensors are looked at for a device."""
+    q, k, v = _z(2, 1, 4, 128), _z(2, 1, 2, 128), _z(2, 1, 2, 128)
+    table = _z(10, 64, dtype=torch.float32)
+    plan = pipeline.NormRope(table, interleaved=what)
+    cache = pipeline.PagedCache(_z(6, 2, 16, 128), _z(6, 2, 16, 128), _z(2, 3, dtype=torch.int32),
+                                _z(2, dtype=torch.int32))
+    grads = pipeline.NormRopeGrads.allocate(q, k)
+    for call in (lambda: pipeline.norm_rope(plan, q, k),
+                 lambda: pipeline.norm_rope_append(plan, q, k, v, None, None, cache),
+                 lambda: pipeline.norm_rope_backward(plan, q, k, q, _z(2, 2, 1, 128), grads)):
+        with pytest.raises(ValueError, match="interleaved"):
+            call()
