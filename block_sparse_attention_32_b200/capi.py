@@ -361,19 +361,24 @@ def msa_index_score_maxpool_e4m3(d: Dims, q_idx8, k_idx8, scale_q, scale_k, pool
 _calls = None
 
 
+def _load_calls():
+    if not os.path.exists(CALLS_PATH):
+        raise RuntimeError(
+            f"{CALLS_PATH} is missing: build it with "
+            "`python -m block_sparse_attention_32_b200.build` (no fallback exists)")
+    spec = importlib.util.spec_from_file_location("msa_calls", CALLS_PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
 def calls():
     """The msa_calls module (raises if it has not been built)."""
     global _calls
     if _calls is None:
         with _lock:
-            if not os.path.exists(CALLS_PATH):
-                raise RuntimeError(
-                    f"{CALLS_PATH} is missing: build it with "
-                    "`python -m block_sparse_attention_32_b200.build` (no fallback exists)")
-            spec = importlib.util.spec_from_file_location("msa_calls", CALLS_PATH)
-            mod = importlib.util.module_from_spec(spec)
-            spec.loader.exec_module(mod)
-            _calls = mod
+            if _calls is None:
+                _calls = _load_calls()
     return _calls
 
 

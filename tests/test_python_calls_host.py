@@ -37,3 +37,26 @@ def test_interleaved_without_a_truth_value_is_refused(what):
                  lambda: pipeline.norm_rope_backward(plan, q, k, q, _z(2, 2, 1, 128), grads)):
         with pytest.raises(ValueError, match="interleaved"):
             call()
+
+
+def test_the_module_is_loaded_once(monkeypatch):
+    """Two first callers at once: one loads it, the other waits and takes the same."""
+    import threading
+    import time
+
+    load, loads = capi.importlib.util.spec_from_file_location, []
+
+    def slow(*a, **kw):
+        loads.append(a)
+        time.sleep(0.2)
+        return load(*a, **kw)
+
+    monkeypatch.setattr(capi, "_calls", None)
+    monkeypatch.setattr(capi.importlib.util, "spec_from_file_location", slow)
+    got = []
+    threads = [threading.Thread(target=lambda: got.append(capi.calls())) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(loads) == 1 and len(got) == 3 and all(m is got[0] for m in got)
