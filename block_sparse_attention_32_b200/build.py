@@ -14,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +23,7 @@ OUT_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(OUT_DIR, "libmsa.so")
 CALLS = os.path.join(OUT_DIR, "msa_calls.so")
 OBJ_DIR = os.path.join(ROOT, "_build", "msa")
+CALLS_TAG = os.path.join(OBJ_DIR, "msa_calls.built_for")
 
 SOURCES = ["msa_api.cu", "index_score.cu", "topk.cu", "block_lists.cu", "block_lists_noalloc.cu",
            "sparse_attn.cu", "sparse_attn_decode.cu", "merge.cu", "recall.cu",
@@ -88,19 +90,35 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def _calls_for() -> str:
+    """What msa_calls.so is bound to: torch's C++ interface and Python's."""
+    import torch
+    return f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')}"
+
+
+def calls_stale() -> bool:
+    """msa_calls.so is missing, older than its sources, or built for another torch or Python."""
+    if _stale(CALLS, [os.path.join(CSRC, "calls.cpp"), os.path.join(ROOT, "include", "msa.h")]):
+        return True
+    try:
+        with open(CALLS_TAG) as f:
+            return f.read() != _calls_for()
+    except OSError:
+        return True
+
+
 def build_calls(force: bool = False) -> str:
     """Compile (if needed) and return the path of msa_calls.so."""
-    src = os.path.join(CSRC, "calls.cpp")
-    if not force and not _stale(CALLS, [src, os.path.join(ROOT, "include", "msa.h")]):
+    if not force and not calls_stale():
         return CALLS
-    import sysconfig
-
     import torch
+    src = os.path.join(CSRC, "calls.cpp")
     troot = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
            "-fvisibility=hidden",
+           f'-DMSA_TORCH_VERSION="{torch.__version__}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-isystem", os.path.join(troot, "include"),
            "-isystem", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
@@ -112,6 +130,9 @@ def build_calls(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS)
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    with open(CALLS_TAG, "w") as f:
+        f.write(_calls_for())
     return CALLS
 
 

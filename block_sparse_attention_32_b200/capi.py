@@ -367,8 +367,16 @@ def _load_calls():
             f"{CALLS_PATH} is missing: build it with "
             "`python -m block_sparse_attention_32_b200.build` (no fallback exists)")
     spec = importlib.util.spec_from_file_location("msa_calls", CALLS_PATH)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
+    rebuild = "build it again with `python -m block_sparse_attention_32_b200.build`"
+    try:
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except ImportError as e:               # libmsa.so missing, or the symbols of another torch
+        raise RuntimeError(f"{CALLS_PATH} does not load ({e}): {rebuild}") from e
+    built_for = getattr(mod, "torch_version", "of another build")
+    if built_for != str(torch.__version__):
+        raise RuntimeError(f"{CALLS_PATH} was built for torch {built_for}, this is "
+                           f"{torch.__version__}: {rebuild}")
     return mod
 
 

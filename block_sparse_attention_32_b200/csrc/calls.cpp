@@ -429,4 +429,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "msa_calls", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_msa_calls() { return PyModule_Create(&module); }
+// torch_version: the torch that the module was compiled for; it serves no other
+PyMODINIT_FUNC PyInit_msa_calls() {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", MSA_TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

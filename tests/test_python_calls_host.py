@@ -60,3 +60,24 @@ def test_the_module_is_loaded_once(monkeypatch):
     for t in threads:
         t.join()
     assert len(loads) == 1 and len(got) == 3 and all(m is got[0] for m in got)
+
+
+def test_a_module_built_for_another_torch_is_refused_and_rebuilt(monkeypatch):
+    """msa_calls.so is bound to the torch whose headers it was compiled with."""
+    assert capi.calls().torch_version == str(torch.__version__)
+    assert not msa_build.calls_stale()
+    monkeypatch.setattr(capi, "_calls", None)
+    monkeypatch.setattr(torch, "__version__", "1.0.0+other")
+    assert msa_build.calls_stale()
+    with pytest.raises(RuntimeError, match="built for torch .*1.0.0.*build"):
+        capi.calls()
+    assert capi._calls is None
+
+
+def test_a_module_that_does_not_load_says_what_to_do(monkeypatch, tmp_path):
+    bad = tmp_path / "msa_calls.so"
+    bad.write_bytes(b"not a library")
+    monkeypatch.setattr(capi, "_calls", None)
+    monkeypatch.setattr(capi, "CALLS_PATH", str(bad))
+    with pytest.raises(RuntimeError, match="does not load.*build"):
+        capi.calls()
