@@ -265,8 +265,9 @@ class HostPipeline:
             self.buf.out, self.buf.lse = self.dev_out[0]
 
 
-def check_device_errors(buf: Buffers):
-    """Raise if any kernel reported a device-side error (synchronises)."""
+def check_device_errors(buf):
+    """Raise if any kernel reported a device-side error (synchronises).  buf: Buffers, or
+    whatever else holds a dev_err (a paged cache, the buffers of decode and window)."""
     code = int(buf.dev_err[0].item())
     if code:
         raise capi.MSAError("device", 0) from RuntimeError(capi.DEVERR.get(code, code))
@@ -348,11 +349,17 @@ def norm_rope_backward(plan: NormRope, q, k, d_q, d_k, grads: NormRopeGrads, pos
 class PagedCache:
     """A paged key-value cache: pages seen as [n_pages, h_kv, page_size, 128] (heads
     or tokens stored outermost), the block table [B, pages per sequence] int32 and
-    the sequences' lengths [B] int32.  Who calls keeps the table and the lengths."""
+    the sequences' lengths [B] int32.  Who calls keeps the table and the lengths.
+    dev_err takes the errors of appends (``check_device_errors(cache)``)."""
     k_pages: torch.Tensor
     v_pages: torch.Tensor
     block_table: torch.Tensor
     seq_lens: torch.Tensor
+    dev_err: torch.Tensor | None = None
+
+    def __post_init__(self):
+        if self.dev_err is None:
+            self.dev_err = torch.zeros((4,), dtype=torch.int32, device=self.k_pages.device)
 
     @staticmethod
     def allocate(batch, max_tokens, h_kv, page_size=64, n_pages=None, tokens_outermost=False,
@@ -395,12 +402,14 @@ def norm_rope_append(plan: NormRope, q, k, v, positions, q_out, cache: PagedCach
                      dev_err=None):
     """norm_rope whose keys, and the values v [B,T,Hk,128], go into the cache's pages
     at positions [B, T] int64 (negative: padding; None: pos0 + i).  The table must
-    already map them; seq_lens is the caller's to advance.  Returns q_out."""
+    already map them: a token without a page leaves the cache as it was and an error in
+    dev_err (the cache's, when not given).  seq_lens is the caller's to advance.  Returns
+    q_out."""
     if q is not None and q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     capi.msa_qk_norm_rope_paged(q, k, v, plan.w_q, plan.w_k, plan.table, q_out, cache.k_pages,
                                 cache.v_pages, cache.block_table, positions, pos0, plan.eps,
-                                plan.interleaved, dev_err)
+                                plan.interleaved, cache.dev_err if dev_err is None else dev_err)
     return q_out
 
 

@@ -81,3 +81,26 @@ def test_a_module_that_does_not_load_says_what_to_do(monkeypatch, tmp_path):
     monkeypatch.setattr(capi, "CALLS_PATH", str(bad))
     with pytest.raises(RuntimeError, match="does not load.*build"):
         capi.calls()
+
+
+def test_the_cache_takes_the_errors_of_appends(monkeypatch):
+    """A page that is not in the table drops keys: without a dev_err of the caller's, the
+    cache's own reports it."""
+    seen = []
+    monkeypatch.setattr(capi, "msa_qk_norm_rope_paged", lambda *a: seen.append(a[-1]))
+    cache = pipeline.PagedCache.allocate(2, 48, 2, page_size=16, device="cpu")
+    made = pipeline.PagedCache(cache.k_pages, cache.v_pages, cache.block_table, cache.seq_lens)
+    plan = pipeline.NormRope(_z(48, 64, dtype=torch.float32))
+    q, k, v = _z(2, 1, 4, 128), _z(2, 1, 2, 128), _z(2, 1, 2, 128)
+    mine = torch.zeros(4, dtype=torch.int32)
+    for c in (cache, made):
+        pipeline.norm_rope_append(plan, q, k, v, None, None, c)
+        pipeline.norm_rope_append(plan, q, k, v, None, None, c, dev_err=mine)
+        assert seen[-2] is c.dev_err and seen[-1] is mine
+        assert c.dev_err.dtype == torch.int32 and c.dev_err.device == c.k_pages.device
+        pipeline.check_device_errors(c)
+        c.dev_err[0] = 5
+        with pytest.raises(capi.MSAError) as e:
+            pipeline.check_device_errors(c)
+        assert "BAD_PAGE" in str(e.value.__cause__)
+    assert cache.dev_err is not made.dev_err
