@@ -288,12 +288,19 @@ def rope_table(n_pos, rot, theta=1.0e6, device="cuda"):
 @dataclasses.dataclass
 class NormRope:
     """What a layer keeps for its per-head norms and rotation: the table (None: no
-    rotation), the norm weights fp32 [d] (None: ones), eps and the pairing."""
+    rotation), the norm weights fp32 [d] (None: ones), eps and the pairing.  dev_err takes
+    the errors of calls that are given none (positions past the table, which leave their
+    rows as they were): ``check_device_errors(plan)``."""
     table: torch.Tensor | None
     w_q: torch.Tensor | None = None
     w_k: torch.Tensor | None = None
     eps: float = 1e-6
     interleaved: bool = False
+    dev_err: torch.Tensor | None = None
+
+    def __post_init__(self):
+        if self.dev_err is None and self.table is not None:
+            self.dev_err = torch.zeros((4,), dtype=torch.int32, device=self.table.device)
 
 
 def norm_rope(plan: NormRope, q, k, q_out=None, k_out=None, positions=None, pos0=0,
@@ -307,7 +314,8 @@ def norm_rope(plan: NormRope, q, k, q_out=None, k_out=None, positions=None, pos0
         k_out = torch.empty((k.shape[0], k.shape[2], k.shape[1], k.shape[3]), dtype=k.dtype,
                             device=k.device)
     capi.msa_qk_norm_rope(q, k, plan.w_q, plan.w_k, plan.table, q_out, k_out, positions, pos0,
-                          plan.eps, plan.interleaved, dev_err)
+                          plan.eps, plan.interleaved,
+                          plan.dev_err if dev_err is None else dev_err)
     return q_out, k_out
 
 
@@ -341,7 +349,8 @@ def norm_rope_backward(plan: NormRope, q, k, d_q, d_k, grads: NormRopeGrads, pos
     ``backward`` gives them).  Returns (dx_q, dx_k, dw_q, dw_k)."""
     capi.msa_qk_norm_rope_bwd(q, k, plan.w_q, plan.w_k, plan.table, d_q, d_k, grads.dx_q,
                               grads.dx_k, grads.dw_q, grads.dw_k, grads.ws, positions, pos0,
-                              plan.eps, plan.interleaved, dev_err)
+                              plan.eps, plan.interleaved,
+                              plan.dev_err if dev_err is None else dev_err)
     return grads.dx_q, grads.dx_k, grads.dw_q, grads.dw_k
 
 

@@ -28,3 +28,20 @@ def test_an_append_to_an_unmapped_page_is_found():
     with pytest.raises(capi.MSAError) as e:
         pipeline.check_device_errors(cache)
     assert "MSA_DEVERR_BAD_PAGE" in str(e.value.__cause__)
+
+
+def test_a_position_past_the_table_is_found():
+    plan = pipeline.NormRope(pipeline.rope_table(10, 64))
+    q, pos = _rn(1, 1, 3, 2, 64), torch.tensor([[3, -1, 9]], device="cuda")
+    pipeline.norm_rope(plan, q, None, positions=pos)
+    gr = pipeline.NormRopeGrads.allocate(q, None)
+    pipeline.norm_rope_backward(plan, q, None, q, None, gr, positions=pos)
+    pipeline.check_device_errors(plan)
+    pos[0, 1] = 10
+    pipeline.norm_rope(plan, q, None, positions=pos)
+    with pytest.raises(capi.MSAError) as e:
+        pipeline.check_device_errors(plan)
+    assert "MSA_DEVERR_BAD_POSITION" in str(e.value.__cause__)
+    plan.dev_err.zero_()
+    pipeline.norm_rope_backward(plan, q, None, q, None, gr, positions=pos)
+    assert int(plan.dev_err[0]) == 4

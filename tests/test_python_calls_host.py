@@ -104,3 +104,22 @@ def test_the_cache_takes_the_errors_of_appends(monkeypatch):
             pipeline.check_device_errors(c)
         assert "BAD_PAGE" in str(e.value.__cause__)
     assert cache.dev_err is not made.dev_err
+
+
+def test_the_plan_takes_the_errors_of_positions(monkeypatch):
+    """A position past the table leaves a row unwritten: reported by the plan's dev_err when
+    the caller gives none."""
+    seen = []
+    monkeypatch.setattr(capi, "msa_qk_norm_rope", lambda *a: seen.append(a[-1]))
+    monkeypatch.setattr(capi, "msa_qk_norm_rope_bwd", lambda *a: seen.append(a[-1]))
+    q, k = _z(2, 1, 4, 128), _z(2, 1, 2, 128)
+    plan = pipeline.NormRope(_z(48, 64, dtype=torch.float32))
+    mine = torch.zeros(4, dtype=torch.int32)
+    grads = pipeline.NormRopeGrads.allocate(q, k)
+    for own, want in ((None, plan.dev_err), (mine, mine)):
+        pipeline.norm_rope(plan, q, k, dev_err=own)
+        pipeline.norm_rope_backward(plan, q, k, q, k, grads, dev_err=own)
+        assert seen[-2] is want and seen[-1] is want
+    pipeline.check_device_errors(plan)
+    # without a table no position is out of range, and there may be no device to tell
+    assert pipeline.NormRope(None).dev_err is None
