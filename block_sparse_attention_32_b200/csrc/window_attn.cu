@@ -349,9 +349,9 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         uint8_t* tile = base + kWaOffRing + slot * 32768;
         if (split || x == 0 || !takes(k - 1)) {          // the tile's first use
           if (!W(WB_KV_FULL + slot, sv / kWaRing)) { ok = false; return; }
-          // keys past the sequence's end may hold anything: their V rows are cleared
-          // (P is 0 there, and 0 * NaN would not be)
-          if (a.kv_len != nullptr && cur->len < a.n_kv)
+          // keys past the sequence's end, or behind the last query, may hold anything: their V
+          // rows are cleared (P is 0 there, and 0 * NaN would not be)
+          if (cur->len < a.n_kv)
             win_clear_keys(tile, *cur, cur->j0 + j, lane);
         }
         if (!begun[x] && no[x] > 0 && !W(WB_O_EMPTY + x, no[x] - 1)) { ok = false; return; }

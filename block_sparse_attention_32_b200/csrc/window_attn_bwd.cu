@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       auto landed = [&](const WbItem& it, int h, int32_t t, uint32_t m) {
         const int s = slot_of(h, m);
         if (!W(XB_STR_FULL + s, use_of(h, m))) return false;
-        if (a.kv_len != nullptr && it.len < a.n_kv && (it.dkv || h == 0)) {
+        if (it.len < a.n_kv && (a.kv_len != nullptr || !it.dkv) && (it.dkv || h == 0)) {
           uint8_t* rows = base + kWbOffStream + s * 32768;
           if (it.dkv)
             win_clear_rows(rows,

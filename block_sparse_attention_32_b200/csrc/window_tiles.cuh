@@ -27,7 +27,7 @@ __device__ __forceinline__ bool elect_one() {
 // 1024-key window.)  Sinks that reach the window make one run from key 0.
 struct WinItem {
   int32_t b, g, i0;          // first query of row tile A
-  int32_t q_pos0, W, len;    // len: min(kv_len[b], n_kv)
+  int32_t q_pos0, W, len;    // len: min(kv_len[b], q_pos0 + n_q)
   int32_t wlo, s_end, nc, nt;
   int32_t j0;                // first tile of this CTA's share (cluster), its nt tiles follow
   int32_t end_a, beg_b;      // last key tile that A sees; first behind the sinks that B sees
@@ -35,11 +35,13 @@ struct WinItem {
   int32_t x0[2], x1[2];      // positions of its first and last such query
 };
 
+// the keys that a query of sequence b can see end here: behind its last token, and behind
+// the last query of the call (a cache may be longer than what has been written)
 __device__ __forceinline__ int32_t win_len(const WindowArgs& a, int32_t b) {
-  const int32_t n = (int32_t)a.n_kv;
+  const int32_t n = (int32_t)(a.q_pos0 + a.n_q);         // <= n_kv
   if (a.kv_len == nullptr) return n;
   const int32_t v = __ldg(a.kv_len + b);
-  if (v < 0 || v > n) report(a.err, MSA_DEVERR_BAD_LENGTH);
+  if (v < 0 || v > a.n_kv) report(a.err, MSA_DEVERR_BAD_LENGTH);
   return max(0, min(v, n));
 }
 
@@ -123,7 +125,7 @@ __device__ __forceinline__ void win_clear_rows(uint8_t* tile, int32_t r0, int32_
   fence_proxy_async_smem();
   __syncwarp();
 }
-// the rows of key tile j at or behind the sequence's end
+// the rows of key tile j at or behind the end of what queries see
 __device__ __forceinline__ void win_clear_keys(uint8_t* tile, const WinItem& it, int j,
                                                int lane) {
   for (int i = 0; i < 4; ++i) {

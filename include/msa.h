@@ -526,8 +526,10 @@ MSA_API msa_status msa_paged_decode_attn(const msa_dims* dims, int64_t window, i
  *          each bf16 of out, so that the fp32 with the bits (out << 16) + (rest << 8)
  *          is o to 2^-17.  The backward's D = dO.o takes it: from the rounded out
  *          alone D is off by up to 2^-8 sum |dO o|, which reaches dq and dk.
- * K and V must be finite at the keys below kv_len.  A stride of 0 over a dimension
- * of extent > 1 (q, k, v; d_o in the backward) is MSA_ERR_UNSUPPORTED. */
+ * K and V must be finite at the keys below min(kv_len, q_pos0 + n_q); what lies
+ * behind them, in a cache longer than what has been written, may be anything.
+ * A stride of 0 over a dimension of extent > 1 (q, k, v; d_o in the backward) is
+ * MSA_ERR_UNSUPPORTED. */
 MSA_API msa_status msa_window_attn_fwd(const msa_dims* dims, int64_t window, int64_t n_sink,
                                        msa_tensor q, msa_tensor k, msa_tensor v,
                                        const int32_t* kv_len, void* out, void* out_rest,

@@ -120,3 +120,36 @@ def test_rows_of_few_keys_keep_one_rounding(B, n, H, G, W, S):
         if few == n:
             for x, e in ((grads[1][b], ek), (grads[2][b], ev)):
                 assert float((x.double() - e).norm() / e.norm()) <= limit
+
+
+@pytest.mark.parametrize("n_q,n_kv,pos0,H,G,W,S,lens", [
+    (64, 2000, 1000, 32, 2, 0, 0, None), (1, 500, 0, 8, 1, 0, 0, None),
+    (130, 700, 300, 8, 2, 70, 5, None), (16, 9000, 8000, 16, 2, 0, 0, None),
+    (300, 1000, 200, 4, 4, 100, 40, [1000, 350]), (40, 300, 100, 16, 2, 3, 1, [140, 139])])
+def test_keys_behind_the_last_query_may_hold_anything(n_q, n_kv, pos0, H, G, W, S, lens):
+    """A cache longer than what has been written: no query sees the keys from q_pos0 + n_q
+    on (nor those from kv_len on), whose K and V may be NaN or infinite."""
+    B = 2
+    q, k, v, d_o = _inputs(B, n_q, n_kv, H, G)
+    kv_len, ends = None, [pos0 + n_q] * B
+    if lens is not None:
+        kv_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        ends = [min(n, pos0 + n_q) for n in lens]
+    for b, n in enumerate(ends):
+        k[b, :, n:], v[b, :, n:] = math.nan, math.nan
+        k[b, :, n:n + 1], v[b, :, n:n + 1] = math.inf, -math.inf
+    buf = _buffers(B, n_q, n_kv, pos0, H, G, W, S)
+    for t in (buf.dq, buf.dk, buf.dv):
+        t.fill_(7.0)
+    out, lse = pipeline.window_forward(buf, q, k, v, kv_len)
+    grads = pipeline.window_backward(buf, q, k, v, d_o, kv_len)
+    assert int(buf.dev_err[0]) == 0
+    scale = 1 / math.sqrt(128)
+    for b, n in enumerate(ends):
+        see = ref.visible(n_q, n_kv, pos0, W, S, n, "cuda")
+        o, l, bound, aux = ref.attention(q[b], k[b], v[b], see, scale)
+        ref.close("o", out[b], o, bound)
+        ref.close_lse(lse[b], l)
+        for x, (e, be) in zip(grads, ref.attention_grads(o, aux, d_o[b], see, scale, G)):
+            ref.close("grad", x[b], e, be, fro=n_q > 1)
+        assert not grads[1][b, :, n:].any() and not grads[2][b, :, n:].any()
