@@ -214,7 +214,8 @@ __device__ __forceinline__ void wb_item(WbItem& it, const WindowBwdArgs& p, int3
     it.len = it.w.len;
   }
   // else it is the row tile whose first rows see at most kWbTwiceKeys keys (dq: one item of
-  // a sequence and group; 8192 tokens, 64 / 8 heads, W = 1024: 1234 us, without 1228)
+  // a sequence and group; one sequence of 8192 tokens, 64 / 8 heads, no window: 1505 us, without
+  // 1493)
   it.half = kTwice || (!it.dkv && it.w.i0 == 0 && a.q_pos0 < kWbTwiceKeys) ? 1 : 0;
   it.nt <<= it.half;
 }
@@ -701,35 +702,43 @@ __global__ void __launch_bounds__(kWbThreads, 1)
             pk[q] = pack_part(u2f(s[2 * q]), u2f(s[2 * q + 1]), kHalf && low);
           tmem_st_32x32b_x16(ts, pk);
         }
+        auto make_ds = [&](auto part) {
+          constexpr bool kPart = kHalf && decltype(part)::value;
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          if (cc == 1) {
-            tmem_ld_32x32b_x16(ts + 16, d);
-            tmem_ld_wait();
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint64_t d0 = nd2, d1 = nd2;
-            if (kDkv) {
-              const ulonglong2 v = m[32 + 4 * cc + q];
-              d0 = v.x;
-              d1 = v.y;
+          for (int cc = 0; cc < 2; ++cc) {
+            if (cc == 1) {
+              tmem_ld_32x32b_x16(ts + 16, d);
+              tmem_ld_wait();
             }
-            const int c = 16 * cc + 4 * q;
-            float e[4];
-            unpack_f32x2(mul_f32x2(pack_f32x2(s[c], s[c + 1]),
-                                   add_f32x2(pack_f32x2(d[4 * q], d[4 * q + 1]), d0)), e[0], e[1]);
-            unpack_f32x2(mul_f32x2(pack_f32x2(s[c + 2], s[c + 3]),
-                                   add_f32x2(pack_f32x2(d[4 * q + 2], d[4 * q + 3]), d1)), e[2],
-                         e[3]);
-            if (!full) {                      // dO.v may be anything where nothing is seen
 #pragma unroll
-              for (int i = 0; i < 4; ++i) e[i] = (vis >> (c + i)) & 1 ? e[i] : 0.f;
+            for (int q = 0; q < 4; ++q) {
+              uint64_t d0 = nd2, d1 = nd2;
+              if (kDkv) {
+                const ulonglong2 v = m[32 + 4 * cc + q];
+                d0 = v.x;
+                d1 = v.y;
+              }
+              const int c = 16 * cc + 4 * q;
+              float e[4];
+              unpack_f32x2(mul_f32x2(pack_f32x2(s[c], s[c + 1]),
+                                     add_f32x2(pack_f32x2(d[4 * q], d[4 * q + 1]), d0)),
+                           e[0], e[1]);
+              unpack_f32x2(mul_f32x2(pack_f32x2(s[c + 2], s[c + 3]),
+                                     add_f32x2(pack_f32x2(d[4 * q + 2], d[4 * q + 3]), d1)),
+                           e[2], e[3]);
+              if (!full) {                      // dO.v may be anything where nothing is seen
+#pragma unroll
+                for (int i = 0; i < 4; ++i) e[i] = (vis >> (c + i)) & 1 ? e[i] : 0.f;
+              }
+              pk[8 * cc + 2 * q] = pack_part(e[0], e[1], kPart && low);
+              pk[8 * cc + 2 * q + 1] = pack_part(e[2], e[3], kPart && low);
             }
-            pk[8 * cc + 2 * q] = pack_part(e[0], e[1], kHalf && low);
-            pk[8 * cc + 2 * q + 1] = pack_part(e[2], e[3], kHalf && low);
           }
-        }
+        };
+        // apart: most steps are not second ones and need no choice between the parts (8192
+        // tokens, 64 / 8 heads, W = 1024: 957 us, with the choice 970)
+        if (kHalf && !low) make_ds(std::false_type{});
+        else make_ds(std::true_type{});
         tmem_st_32x32b_x16(ts + 16, pk);
         tmem_st_wait();
         tc_fence_before();
