@@ -19,8 +19,8 @@
 // cosines and sines (fp32, the size of two bf16 rows) are read once per hc heads
 // and kept in registers.  Everything is computed in fp32 and rounded to bf16 once,
 // at the store.
-// Measured: forward, 32768 tokens x (32 + 8) heads of 128: 110 us, 688 MB, 6.2 TB/s
-// (0.95 of the copy rate).  Backward, 16384 x (64 + 8), bf16 gradients: 160 us, 915
+// Measured: forward, 32768 tokens x (32 + 8) heads of 128: the kernel alone 110 us, 688
+// MB, 6.2 TB/s (0.95 of the copy rate), a call after another 117 to 124.  Backward, 16384 x (64 + 8), bf16 gradients: 160 us, 915
 // MB, 5.7 TB/s (0.87; the shuffles, unpacking and the two sums a row keep it from the
 // rest).  64 tokens of a decode step into their pages: 5 us, a launch and a latency.
 #include "common.cuh"

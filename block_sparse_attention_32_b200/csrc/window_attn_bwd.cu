@@ -140,9 +140,12 @@ WbPlan wb_plan(const WindowArgs& a) {
   if (a.window > 0) keys = min64(keys, min64(a.window, keys) + a.sink);
   p.twice = total * keys <= kWbTwiceTerms || keys <= kWbTwiceKeys;
   total *= a.batch * a.G;
-  // Tiles of a chunk: few while SMs stand idle (512 tokens, 8 / 1 heads, no window: 4 tiles
-  // 46 us, 8: 52, 32: 83), then about 1.6 chunks an SM (1024 tokens, 16 / 2 heads: 62 us, with
-  // one an SM 69, with 32 tiles 97; 3 ragged x 1111: 109, with two an SM 115), up to 32 tiles
+  // Tiles of a chunk: at least 4 (where they come twice, 2), few while SMs stand idle (512
+  // tokens, 8 / 1 heads, no window: 4 tiles 46 us, 8: 52, 32: 83); then a 90th of all tiles,
+  // 0.6 chunks an SM, up to 32.  More and shorter chunks fill the SMs, and leave more fp32
+  // sums to be added: with a 74th, 90th, 120th, 148th (one an SM), 3 ragged x 1111 tokens
+  // take 115, 109, 105, 105 us, 1024 tokens of 16 / 2 heads 62, 62, 66, 69 (with 32 tiles 97).
+  // Past 32 * 296 tiles a chunk is a 296th: two an SM at most, which bounds the workspace.
   p.chunk = (int32_t)max64(max64(p.twice ? 2 : 4, min64(32, (total + 89) / 90)),
                            (total + 295) / 296);
   p.c_lo = p.nblk;
