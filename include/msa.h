@@ -545,11 +545,12 @@ MSA_API msa_status msa_window_attn_fwd(const msa_dims* dims, int64_t window, int
  *   dk, dv       [B, h_kv, n_kv, 128] bf16, contiguous, 32-byte aligned
  *   ws           msa_window_attn_bwd_workspace() bytes, 32-byte aligned
  * P and dS enter the sums as bf16 (2^-8 of each term), or in two parts that keep
- * 2^-17: in every sum where window + n_sink <= 4 (window > 0) and for short sequences (of at
- * most about 128 tokens, a few hundred with a window of 64 or less), and in dq for
- * the queries of a sequence that see at most 4 keys.  Which of them depends on the
- * sequence's shape (n_q, n_kv, q_pos0, window, n_sink, h_q / h_kv), not on the batch or on
- * the number of groups.  A query that sees one key gets dq = 0 exactly.
+ * 2^-17: in every sum where window + n_sink <= 4 (window > 0) and for short sequences
+ * (up to some 150 to 350 tokens, the fewer the more heads a group has; a few hundred with
+ * a window of 64 or less), and in dq for the queries of a sequence that see at most 4
+ * keys.  Which of them depends on the sequence's shape (n_q, n_kv, q_pos0, window, n_sink,
+ * h_q / h_kv), not on the batch or on the number of groups.  A query that sees one key
+ * gets dq = 0 exactly.
  * All three are summed in fp32 and rounded to bf16 once; padded queries get
  * dq = 0 and add nothing, keys that nobody sees get 0.  Bit-identical from run to
  * run. */
